@@ -344,7 +344,8 @@ int wpk_get_trace(wpk_handle *h, void *host_buf, size_t bytes);
 int wpk_get_error_info(wpk_handle *h, wpk_error_info *info);
 
 /* Human-readable message for the last failing call on this handle; with
- * h == NULL, the message of this thread's last failed wpk_build_graph. */
+ * h == NULL, the message of this thread's last failed call without a handle
+ * (wpk_build_graph, the wpk_kv4_* operators, wpk_sample). */
 const char *wpk_last_error(const wpk_handle *h);
 
 /* Stop the resident grid (if any), release library-owned tables, free h. */
@@ -404,6 +405,111 @@ int wpk_set_active_slots(wpk_handle *h, const int32_t *active, int n);
  * Inputs, outputs and errors are those of wpk_step. */
 int wpk_step_noalloc(wpk_handle *h, const int32_t *in_tok_dev, int32_t *out_tok_dev, float *logits_dev,
                      void *stream);
+
+/* ------------------------------------------------- a paged cache in 4 bits */
+/* Element types of the operators' tensors. */
+enum { WPK_F32 = 0, WPK_BF16 = 1, WPK_F16 = 2 };
+
+/* A paged KV cache held in 4 bits (one layer's).  Each row - the K or the V of
+ * one token and kv head, head_dim values - is held as 4-bit codes c with a
+ * scale s and an offset z (bf16 each), x ~ s c + z:
+ *   z = the largest bf16 number <= min x,
+ *   s = the bf16 number next to (max x - z) / 15 (ties to even),
+ *   c = (x - z) / s rounded to a whole number (ties to even), within 0..15
+ *       (0 where s is 0);
+ * the codes are those of exact arithmetic.  A row with a NaN or an infinity
+ * reads back as NaN.  A row takes head_dim / 2 + 4 bytes (36 of the 128 that
+ * bf16 takes at head_dim 64).
+ *
+ * pages_dev: [n_blocks][n_kv_heads][page], a page of wpk_kv4_page_bytes bytes:
+ * K codes [page_tokens][head_dim / 2], V codes, K (s, z) [page_tokens], V
+ * (s, z).  Word j of a row's codes holds dims 4j .. 4j + 3 in its low half and
+ * head_dim / 2 + 4j .. + 3 in its high half, lowest nibble first.
+ * block_table_dev: [batch][max_blocks] page ids; an id outside [0, n_blocks)
+ * names no page.  head_dim is 64 or 128, page_tokens a multiple of 16, <= 256.
+ * The caller owns both buffers; pages_dev is 16-byte aligned.
+ *
+ * Rows of a call: sequence b brings the tokens indptr_dev[b] ..
+ * indptr_dev[b + 1] - 1 (int32 [batch + 1], increasing) of `total`; NULL =
+ * total / batch tokens each.  Its first one has position pos_dev[b] (the tokens
+ * it holds already), the next one pos_dev[b] + 1, ...  A sequence with
+ * pos_dev[b] < 0 is idle.  A position has no place when its page has none, or
+ * past max_blocks pages, or (where a rope table is given) past that table.
+ * Rows from indptr_dev[batch] on are left as they were.
+ *
+ * rope_dev: (cos, sin) fp32 pairs [rope_positions][head_dim / 2] that turn the
+ * pair (i, i + head_dim / 2) of a row at its position; NULL = no rotation.
+ *
+ * Tensors are [token][head][head_dim] with a contiguous last dimension;
+ * strides are in elements, multiples of 4, and pointers aligned to 4 elements.
+ * The calls are stream-ordered, allocate nothing, keep nothing between calls
+ * and can be captured.  Messages of failed calls: wpk_last_error(NULL). */
+typedef struct wpk_kv4_cache {
+  void *pages_dev;
+  const int32_t *block_table_dev;
+  int64_t n_blocks;
+  int batch, max_blocks, n_kv_heads, head_dim, page_tokens;
+} wpk_kv4_cache;
+
+/* Bytes of one page of one kv head; pages_dev takes n_blocks * n_kv_heads of
+ * them. */
+int wpk_kv4_page_bytes(int head_dim, int page_tokens, int64_t *bytes);
+
+/* Append rows: K rotated to its position (rope_dev) and V, quantised.  The
+ * rotation is computed in 64 bits.  Rows without a place are dropped.  Two rows
+ * of one call must not share a place (tables that share pages may only share
+ * pages that this call does not write). */
+int wpk_kv4_append(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32_t *indptr_dev, int total,
+                   const void *k_dev, int64_t k_token_stride, int64_t k_head_stride, const void *v_dev,
+                   int64_t v_token_stride, int64_t v_head_stride, int dtype, const float *rope_dev,
+                   int rope_positions, void *stream);
+
+/* Read rows back: s c + z, rounded to dtype.  A row without a place, or of an
+ * idle sequence, reads as zeros. */
+int wpk_kv4_read(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32_t *indptr_dev, int total, void *k_dev,
+                 int64_t k_token_stride, int64_t k_head_stride, void *v_dev, int64_t v_token_stride,
+                 int64_t v_head_stride, int dtype, void *stream);
+
+/* Attention of new tokens over the cache that already holds them: the query at
+ * position p sees the keys 0 .. p of its sequence that have a place;
+ * out = softmax(scale q K^T) V in dtype, query heads h reading kv head
+ * h / (n_heads / n_kv_heads).  scale 0 = 1 / sqrt(head_dim).  max_new: an upper
+ * bound of the tokens of any one sequence (rows past it are left as they
+ * were).  rope_dev rotates q on the way.  A query that sees no key, one past
+ * the rope table and one of an idle sequence answer zeros. */
+int wpk_kv4_attention(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32_t *indptr_dev, int total,
+                      int max_new, const void *q_dev, int64_t q_token_stride, int64_t q_head_stride, int n_heads,
+                      int dtype, const float *rope_dev, int rope_positions, float scale, void *out_dev,
+                      int64_t out_token_stride, int64_t out_head_stride, void *stream);
+
+/* ----------------------------------------------------- the next token */
+/* Draw a token per row of logits [batch][vocab] (dtype; row_stride elements
+ * between rows, the last dimension contiguous) with the given uniform numbers
+ * uniform_dev[b] in [0, 1).  temperature_dev, top_k_dev, top_p_dev and
+ * min_p_dev are [batch] or NULL (off).  With zmax the row's largest logit,
+ * w_i = exp((z_i - zmax) / temperature) in 64 bits, tokens ranked by logit,
+ * equal ones by id:
+ *   top-k  keeps the first top_k tokens (off where <= 0);
+ *   top-p  of those, keeps the shortest beginning whose mass (sum of w) is at
+ *          least top_p of theirs, one token at least (off where not < 1);
+ *   min-p  of those, keeps the tokens with w >= min_p (off where not > 0; a
+ *          min_p above 1 counts as 1);
+ *   the token is the first one in the order of ids at which the kept mass
+ *          summed up is above uniform_dev[b] times all of it.
+ * A temperature that is not > 0 takes the largest logit, the lowest id of equal
+ * ones.  A logit of -inf masks its token.  A row with a NaN or +inf, or with
+ * nothing but -inf, answers token -1, log-probability NaN and 0 kept tokens.
+ * Masses are summed as whole multiples of 2^-45, so the result does not depend
+ * on the order of the sums.  vocab <= 262144.
+ *   out_tok_dev     int32 [batch] (may be the in_tok_dev of the next wpk_step)
+ *   out_logprob_dev fp32 [batch] or NULL: log of the token's share of the kept
+ *                   mass
+ *   out_kept_dev    int32 [batch] or NULL: tokens kept
+ * Stream-ordered; allocates nothing, keeps nothing between calls and can be
+ * captured.  Messages of failed calls: wpk_last_error(NULL). */
+int wpk_sample(const void *logits_dev, int dtype, int batch, int vocab, int64_t row_stride, const float *uniform_dev,
+               const float *temperature_dev, const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev,
+               int32_t *out_tok_dev, float *out_logprob_dev, int32_t *out_kept_dev, void *stream);
 
 /* Check of the tensor-core tile (tests): D[128][N] = A . (B1 + B2)^T with fp32
  * accumulation, computed by one CTA through the same path as the program's

@@ -5,6 +5,7 @@ The compute path is ``libwpk.so`` (CUDA, built in-tree by
 """
 from .wpk import (  # noqa: F401
     Engine,
+    KV4Cache,
     OP_NAMES,
     TRACE_DTYPE,
     WPK_MEGAKERNEL,
@@ -13,6 +14,8 @@ from .wpk import (  # noqa: F401
     load_library,
     model_cfg,
     plan_cfg,
+    rope_table,
+    sample,
     wpk_build_graph,
     wpk_debug_break_counter,
     wpk_destroy,

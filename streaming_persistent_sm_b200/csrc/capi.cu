@@ -148,7 +148,7 @@ struct wpk_handle {
 
 namespace {
 
-thread_local std::string g_build_error;  // message of the last failed wpk_build_graph
+thread_local std::string g_build_error;  // message of the last failed call without a handle
 
 int fail(wpk_handle* h, int code, const std::string& msg) {
   if (h) h->err = msg;
@@ -668,6 +668,16 @@ int launch_prefill(wpk_handle* h, PrefillProgram* prog, const int32_t* tokens, i
 const CompiledGraph& selected_graph(const wpk_handle* h) { return h->selected ? h->selected->g : h->g; }
 
 }  // namespace
+
+namespace wpk {
+int op_fail(int code, const char* msg) noexcept {
+  try {
+    g_build_error = msg;
+  } catch (...) {  // no memory for the message: the code says enough
+  }
+  return code;
+}
+}  // namespace wpk
 
 extern "C" {
 
