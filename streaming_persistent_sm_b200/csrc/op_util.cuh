@@ -54,6 +54,13 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The same in two halves, for whole CTAs between which other work goes on.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // Reads of another CTA's shared memory: the address in this CTA, the rank.
 __device__ __forceinline__ uint32_t cluster_address(const void* p, int rank) {
   uint32_t a;
