@@ -87,16 +87,11 @@ __device__ __forceinline__ double exp_neg(double t) {
   double r = fma(k, -0.69314718055994529, t);
   r = fma(k, -2.3190468138462996e-17, r);  // ln 2 less its double
   r *= 0.25;
-  double p = 1.0 / 362880.0;
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
+  // pairs of terms, so that few depend on one another
+  const double r2 = r * r, r4 = r2 * r2;
+  const double p0 = 1.0 + r, p1 = fma(r, 1.0 / 6.0, 0.5), p2 = fma(r, 1.0 / 120.0, 1.0 / 24.0),
+               p3 = fma(r, 1.0 / 5040.0, 1.0 / 720.0), p4 = fma(r, 1.0 / 362880.0, 1.0 / 40320.0);
+  double p = fma(fma(r4, p4, fma(r2, p3, p2)), r4, fma(r2, p1, p0));
   p *= p;
   p *= p;
   return __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
@@ -238,19 +233,6 @@ __device__ __forceinline__ uint64_t block_before(SampleShared& S, uint64_t v) {
   return upto - v + warp_sum64(lane < warp ? S.warp_a[lane] : 0);
 }
 
-// The same over one warp, or over the CTA.
-template <bool kBlock>
-__device__ __forceinline__ uint64_t sum_before(SampleShared& S, uint64_t v) {
-  return kBlock ? block_before(S, v) : warp_scan64(v) - v;
-}
-template <bool kBlock>
-__device__ __forceinline__ uint64_t sum_all(SampleShared& S, uint64_t v) {
-  if (!kBlock) return warp_sum64(v);
-  uint64_t same = 0;
-  block_join<false>(S, &v, &same);
-  return v;
-}
-
 constexpr int kEach = kList / kSampThreads;  // entries of the list that a thread holds
 static_assert(kEach == 4, "sort_each holds four");
 
@@ -317,75 +299,230 @@ struct Filters {
   double u;
 };
 
-// The rest of a row on the first CTA, from its m candidates: a beginning of the
-// ranking that holds all that can be kept.  all_mass: that of the whole row, for
-// top-p without top-k.
-template <bool kBlock>
-__device__ __forceinline__ void finish(SampleShared& S, const SampleArgs& A, int b, const Weigh& W, const Filters& f,
-                                       int m, uint64_t all_mass) {
-  const int i0 = kEach * threadIdx.x;
-  uint64_t v[kEach], w[kEach], sum = 0;
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) v[e] = i0 + e < m ? S.list[i0 + e] : kAll;
-  sort_each(S, v, sort_size(m));
+// An answer, by one thread.
+__device__ __forceinline__ void answer(const SampleArgs& A, int b, const Weigh& W, uint32_t id, float z, uint64_t mass,
+                                       int kept) {
+  A.tok[b] = (int)id;
+  if (A.logprob) {
+    const double t = ((double)z - (double)W.zmax) * W.inv_t;
+    A.logprob[b] = (float)(t - log((double)mass / kOne));
+  }
+  if (A.kept) A.kept[b] = kept;
+}
+__device__ __forceinline__ float logit_of(uint64_t place) { return from_rank(~(uint32_t)(place >> 32)); }
+
+// What a CTA does with few tokens: four lanes a token go through all of them
+// and add up what comes before it - 128 * 128 comparisons, no order made.
+constexpr int kFew = kSampThreads / 4;
+__device__ __forceinline__ uint64_t four_sum(uint64_t v) {
+  v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+  return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+}
+
+// The draw among n <= kFew tokens: places in S.list, in S.local twice their mass
+// and 1 where they are kept.
+__device__ __forceinline__ void draw_few(const SampleShared& S, const SampleArgs& A, int b, const Weigh& W, double u,
+                                         int n) {
+  const int e = threadIdx.x >> 2;
+  const uint64_t mine = e < n ? S.list[e] : 0, own = e < n ? S.local[e] : 0;
+  uint64_t mass = 0, kept = 0, before = 0;
+#pragma unroll 2
+  for (int j = threadIdx.x & 3; j < n; j += 4) {
+    const uint64_t w = (S.local[j] & 1) ? S.local[j] >> 1 : 0;
+    mass += w;
+    kept += S.local[j] & 1;
+    if ((uint32_t)S.list[j] < (uint32_t)mine) before += w;
+  }
+  mass = four_sum(mass);
+  kept = four_sum(kept);
+  before = four_sum(before);
+  const uint64_t want = min((uint64_t)(u * (double)mass), mass - 1);
+  if ((threadIdx.x & 3) == 0 && (own & 1) && before <= want && want - before < own >> 1)
+    answer(A, b, W, (uint32_t)mine, logit_of(mine), mass, (int)kept);
+}
+
+// The rest of a row from its n <= kFew candidates: a beginning of the ranking
+// that holds all that can be kept.  all_mass: that of the whole row, for top-p
+// without top-k.
+__device__ __forceinline__ void finish_few(SampleShared& S, const SampleArgs& A, int b, const Weigh& W,
+                                           const Filters& f, int n, uint64_t all_mass) {
+  const int e = threadIdx.x >> 2;
+  if (threadIdx.x < n) S.local[threadIdx.x] = W.mass(logit_of(S.list[threadIdx.x])) << 1;
+  __syncthreads();
+  const uint64_t mine = e < n ? S.list[e] : 0, own = e < n ? S.local[e] >> 1 : 0;
+  uint64_t rank = 0, before = 0;
+#pragma unroll 2
+  for (int j = threadIdx.x & 3; j < n; j += 4)
+    if (S.list[j] < mine) {
+      ++rank;
+      before += S.local[j] >> 1;
+    }
+  rank = four_sum(rank);
+  before = four_sum(before);
+  bool keep = !f.by_k || rank < (uint64_t)f.k;
+  if (f.by_p) {
+    if (f.by_k) {  // the mass that top-k leaves
+      __syncthreads();
+      if ((threadIdx.x & 3) == 0 && e < n) S.local[e] = own << 1 | keep;
+      __syncthreads();
+      all_mass = 0;
+      for (int j = threadIdx.x & 3; j < n; j += 4)
+        if (S.local[j] & 1) all_mass += S.local[j] >> 1;
+      all_mass = four_sum(all_mass);
+    }
+    // kept while what comes before falls short of the share
+    keep = keep && (before == 0 || (double)before < (double)f.p * (double)all_mass);
+  }
+  if (f.floor_w > 0.0) keep = keep && W.weight(logit_of(mine)) >= f.floor_w;
+  __syncthreads();
+  if ((threadIdx.x & 3) == 0 && e < n) S.local[e] = own << 1 | keep;
+  __syncthreads();
+  draw_few(S, A, b, W, f.u, n);
+}
+
+// Among the n tokens of the list (kFew < n <= kList; whole CTAs) that `upto`
+// does not leave out: the place of the last one of the shortest beginning whose
+// number (or mass) reaches `target`, which all of them together do.  They fall
+// into 1024 bins by the bits of their logits; the ones of the border's bin are
+// compared with one another.
+__device__ __forceinline__ uint64_t select(SampleShared& S, const Weigh& W, int n, bool by_mass, uint64_t target,
+                                           uint64_t upto) {
+  uint64_t least = kAll, most = kAll;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kSampThreads) {
+    const uint32_t r = ~(uint32_t)(S.list[i] >> 32);
+    least = min(least, (uint64_t)r);
+    most = min(most, (uint64_t)~r);
+  }
+  block_join<true>(S, &least, &most);
+  const uint32_t lo = (uint32_t)least, hi = ~(uint32_t)most;
+  for (int i = threadIdx.x; i < kLocal; i += kSampThreads) S.local[i] = 0;
+  if (threadIdx.x == 0) S.local_n = 0;
+  __syncthreads();
+  auto bin_of = [&](uint64_t key) {
+    return (int)((uint64_t)(hi - ~(uint32_t)(key >> 32)) * kLocal / ((uint64_t)(hi - lo) + 1));
+  };
+  auto worth = [&](uint64_t key) { return by_mass ? W.mass(logit_of(key)) : (uint64_t)1; };
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kSampThreads) {
+    const uint64_t key = S.list[i];
+    if (key <= upto)
+      atomicAdd(reinterpret_cast<unsigned long long*>(&S.local[bin_of(key)]), (unsigned long long)worth(key));
+  }
+  __syncthreads();
+  {
+    static_assert(kLocal == 2 * kSampThreads, "two bins a thread");
+    const uint64_t v0 = S.local[2 * threadIdx.x], v1 = S.local[2 * threadIdx.x + 1];
+    const uint64_t left = block_before(S, v0 + v1);
+    if (left < target && target <= left + v0 + v1) {
+      const bool second = target > left + v0;
+      S.found = 2 * threadIdx.x + second;
+      S.warp_b[0] = left + (second ? v0 : 0);
+    }
+  }
+  __syncthreads();
+  const int bin = S.found;
+  target -= S.warp_b[0];
+  // its tokens, together (as many as there is room for)
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kSampThreads) {
+    const uint64_t key = S.list[i];
+    if (key <= upto && bin_of(key) == bin) {
+      const uint32_t at = atomicAdd(&S.local_n, 1u);
+      if (at < kLocal) S.local[at] = key;
+    }
+  }
+  __syncthreads();
+  const int in = (int)S.local_n;
+  const bool all = in > kLocal;  // else go through the whole list
+  const int m = all ? n : in;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < m; i += kSampThreads) {
+    const uint64_t key = all ? S.list[i] : S.local[i];
+    if (all && !(key <= upto && bin_of(key) == bin)) continue;
+    uint64_t before = 0;
+#pragma unroll 1
+    for (int j = 0; j < m && before < target; ++j) {
+      const uint64_t other = all ? S.list[j] : S.local[j];
+      if (other < key && (!all || (other <= upto && bin_of(other) == bin))) before += worth(other);
+    }
+    if (before < target && target <= before + worth(key)) S.warp_b[1] = key;
+  }
+  __syncthreads();
+  return S.warp_b[1];
+}
+
+// The rest of a row from its n candidates, kFew < n <= kList (whole CTAs).
+__device__ __forceinline__ void finish_many(SampleShared& S, const SampleArgs& A, int b, const Weigh& W,
+                                            const Filters& f, int n, uint64_t all_mass) {
+  uint64_t upto = kAll;
+#pragma unroll 1
+  for (int by_mass = 0; by_mass < 2; ++by_mass) {
+    if (by_mass ? !f.by_p : !f.by_k) continue;
+    uint64_t target = (uint64_t)f.k;
+    if (by_mass) {
+      uint64_t in = 0, same = 0;  // the mass that is in the list, up to top-k's border
+#pragma unroll 1
+      for (int i = threadIdx.x; i < n; i += kSampThreads)
+        if (S.list[i] <= upto) in += W.mass(logit_of(S.list[i]));
+      block_join<false>(S, &in, &same);
+      const double want = ceil((double)f.p * (double)(f.by_k ? in : all_mass));
+      target = want > 1.0 ? (uint64_t)want : (uint64_t)1;
+      if (target > in) continue;  // all of the list (min-p ends it)
+    }
+    if (by_mass || target < (uint64_t)n) upto = select(S, W, n, by_mass, target, upto);
+  }
+  // the kept ones together
+  __syncthreads();
+  if (threadIdx.x == 0) S.local_n = 0;
+  __syncthreads();
+  uint64_t key[kEach], mass = 0, kept = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    w[e] = i0 + e < m ? W.mass(from_rank(~(uint32_t)(v[e] >> 32))) : 0;
-    sum += w[e];
+    const int i = e * kSampThreads + threadIdx.x;
+    key[e] = i < n ? S.list[i] : kAll;
+    const bool on = i < n && key[e] <= upto && (f.floor_w == 0.0 || W.weight(logit_of(key[e])) >= f.floor_w);
+    if (!on) key[e] = kAll;
+    if (on) mass += W.mass(logit_of(key[e]));
+    kept += on;
   }
-  // how many are kept: top-k's number, top-p's beginning of it, min-p's
-  int keep = f.by_k ? min(m, f.k) : m;
-  if (f.by_p) {
-    if (f.by_k) {
-      uint64_t in = 0;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (i0 + e < keep) in += w[e];
-      all_mass = sum_all<kBlock>(S, in);
-    }
-    const double want = ceil((double)f.p * (double)all_mass);
-    const uint64_t target = want > 1.0 ? (uint64_t)want : (uint64_t)1;
-    uint64_t left = sum_before<kBlock>(S, sum), short_of = 0;  // beginnings that fall short
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      left += w[e];
-      short_of += i0 + e < keep && left < target;
-    }
-    keep = min(keep, (int)sum_all<kBlock>(S, short_of) + 1);
-  }
-  if (f.floor_w > 0.0) {
-    uint64_t heavy = 0;
+  block_join<false>(S, &mass, &kept);  // every key is read
+  if (kept <= kFew) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
-      heavy += i0 + e < keep && W.weight(from_rank(~(uint32_t)(v[e] >> 32))) >= f.floor_w;
-    keep = (int)sum_all<kBlock>(S, heavy);
+      if (key[e] != kAll) {
+        const uint32_t at = atomicAdd(&S.local_n, 1u);
+        S.list[at] = key[e];
+        S.local[at] = W.mass(logit_of(key[e])) << 1 | 1;
+      }
+    __syncthreads();
+    draw_few(S, A, b, W, f.u, (int)kept);
+    return;
   }
-  // the kept ones in the order of ids, and the draw
-  uint64_t in = 0;
+  // many: in the order of ids
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (key[e] != kAll) {
+      const uint32_t at = atomicAdd(&S.local_n, 1u);
+      S.list[at] = key[e] << 32 | key[e] >> 32;
+    }
+  __syncthreads();
+  uint64_t sum = 0, w[kEach];
+  const int i0 = kEach * threadIdx.x;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) key[e] = i0 + e < (int)kept ? S.list[i0 + e] : kAll;
+  sort_each(S, key, sort_size((int)kept));
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const bool on = i0 + e < keep;
-    if (on) in += w[e];
-    v[e] = on ? v[e] << 32 | v[e] >> 32 : kAll;
-  }
-  const uint64_t mass = sum_all<kBlock>(S, in);
-  const uint64_t want = min((uint64_t)(f.u * (double)mass), mass - 1);
-  sort_each(S, v, sort_size(keep));
-  sum = 0;
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    w[e] = i0 + e < keep ? W.mass(from_rank(~(uint32_t)v[e])) : 0;
+    w[e] = i0 + e < (int)kept ? W.mass(from_rank(~(uint32_t)key[e])) : 0;
     sum += w[e];
   }
-  uint64_t left = sum_before<kBlock>(S, sum);
+  uint64_t left = block_before(S, sum);
+  const uint64_t want = min((uint64_t)(f.u * (double)mass), mass - 1);
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    if (left <= want && want < left + w[e]) {  // in one thread
-      const double t = ((double)from_rank(~(uint32_t)v[e]) - (double)W.zmax) * W.inv_t;
-      A.tok[b] = (int)(v[e] >> 32);
-      if (A.logprob) A.logprob[b] = (float)(t - log((double)mass / kOne));
-      if (A.kept) A.kept[b] = keep;
-    }
+    if (left <= want && want < left + w[e])  // in one thread
+      answer(A, b, W, (uint32_t)(key[e] >> 32), from_rank(~(uint32_t)key[e]), mass, (int)kept);
     left += w[e];
   }
 }
@@ -399,6 +536,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   const int base = min(A.vocab, rank * A.slice), n = min(A.vocab - base, A.slice);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int turn = 0;
+  // the row's settings, asked for before its logits
+  const float temperature = A.temperature ? A.temperature[b] : 1.f, u_part = A.uniform[b];
+  const float p = A.top_p ? A.top_p[b] : 1.f, mp = A.min_p ? A.min_p[b] : 0.f;
+  const int k = A.top_k ? A.top_k[b] : 0;
 
   // read the slice, padded with masked tokens to whole vectors of all lanes
   const int padded = (n + 127) & ~127;
@@ -458,7 +599,6 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   // a warp's tokens, in the order of ids: whole vectors of all lanes
   const int per = ((padded + kSampWarps - 1) / kSampWarps + 127) & ~127;
   const int seg_lo = min(padded, warp * per), seg_hi = min(padded, seg_lo + per);
-  const float temperature = A.temperature ? A.temperature[b] : 1.f;
   const bool none = bad != 0 || finite == 0;
   if (none || !(temperature > 0.f)) {  // as for every CTA of the cluster
     // the lowest id of the largest logit
@@ -487,24 +627,21 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   W.log2_t = (float)log2_t;
   W.log2_t_rest = isfinite(W.log2_t) ? (float)(log2_t - (double)W.log2_t) : 0.f;
   Filters f;
-  f.k = A.top_k ? A.top_k[b] : 0;
-  f.p = A.top_p ? A.top_p[b] : 1.f;
-  const float mp = A.min_p ? A.min_p[b] : 0.f;
+  f.k = k;
+  f.p = p;
+  f.by_k = k > 0 && (uint32_t)k < finite;
+  f.by_p = p < 1.f;
   f.floor_w = mp > 0.f ? fmin((double)mp, 1.0) : 0.0;
-  const float u_part = A.uniform[b];
   f.u = u_part > 0.f ? fmin((double)u_part, 1.0) : 0.0;
-  f.by_k = f.k > 0 && (uint32_t)f.k < finite;
-  f.by_p = f.p < 1.f;
   const bool by_k = f.by_k, by_p = f.by_p;
-  const float p = f.p;
-  const int k = f.k;
   const double floor_w = f.floor_w;
   const bool filtered = by_k || by_p || floor_w > 0.0;
 
   // The mass of all tokens: what a row without filters draws from, and top-p
-  // alone is measured by.  For the latter, heavy tokens' weights in units of
-  // 2^-13, rounded down, are summed up in buckets of their log2.
-  constexpr float kSteps = kBins / kTail;
+  // alone is measured by.  For the latter, tokens fall into buckets of 1/48 of
+  // their weights' log2; a bucket sums up 2^16 times what its tokens weigh
+  // against its near edge, rounded down (1 - x ln 2 <= 2^-x).
+  constexpr float kSteps = 48.f;
   uint64_t all_mass = 0;
   if (!filtered || (by_p && !by_k)) {
     uint64_t v = 0;
@@ -512,19 +649,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
     for (int i = seg_lo + 4 * lane; i < seg_hi; i += 128) {
       const float4 x4 = *reinterpret_cast<const float4*>(z + i);
       const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-      const float t_top = W.log2_weight(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-      if (t_top < -kTail) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v += W.tail_mass(x[e], W.log2_weight(x[e]));
-      } else {
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          const float xe = e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3];
-          const uint64_t u = W.mass(xe);
-          v += u;
-          const float t = W.log2_weight(xe);
-          if (filtered && !(t < -kTail) && xe > -INFINITY)
-            atomicAdd(&S.count[bucket(-t * kSteps)], (uint32_t)(u >> 32));
+      for (int e = 0; e < 4; ++e) {
+        const float t = W.log2_weight(x[e]);
+        if (t < -kTail)
+          v += W.tail_mass(x[e], t);
+        else if (x[e] > -INFINITY)
+          v += W.heavy_mass(x[e]);
+        if (filtered) {
+          const float at = fmaxf(-t, 0.f) * kSteps, edge = floorf(at);  // a NaN is 0
+          if (at < (float)kBins) atomicAdd(&S.count[(int)edge], (uint32_t)(65536.f - (at - edge) * (45426.1f / kSteps)));
         }
       }
     }
@@ -554,12 +688,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
               uint64_t left = upto - four;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                if (left <= rest && rest < left + u[e]) {  // in one lane
-                  const double t = ((double)z[i + e] - (double)W.zmax) * W.inv_t;
-                  A.tok[b] = base + i + e;
-                  if (A.logprob) A.logprob[b] = (float)(t - log((double)all_mass / kOne));
-                  if (A.kept) A.kept[b] = (int)finite;
-                }
+                if (left <= rest && rest < left + u[e])  // in one lane
+                  answer(A, b, W, (uint32_t)(base + i + e), z[i + e], all_mass, (int)finite);
                 left += u[e];
               }
               break;
@@ -573,9 +703,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
     }
   }
 
+  // What is kept: tokens up to place `upto`, of weight floor_w at least.
+  uint64_t upto = kAll;
+  bool known = false;  // upto is
   {
-    // the candidates: tokens no further than `reach` from the largest logit
+    // the candidates: tokens no further than `reach` from the largest logit, or
+    // (flat rows under top-p alone) those of the border's buckets
     float reach = INFINITY;
+    int border_bin = -1;
     if (by_k || by_p) {
       if (by_k) {
         // the k-th best of the maxima of four tokens each: at least k tokens are
@@ -591,50 +726,87 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
       // rank 0 sums the CTAs' buckets and finds the one that reaches the target
       turn ^= 1;
       if (rank == 0) {
-        const double want = ceil((double)p * (double)all_mass / 4294967296.0);
-        const uint64_t target = by_k ? (uint64_t)k : want > 1.0 ? (uint64_t)want : 1;
-        uint32_t c[kEach];
+        uint32_t got[kMaxCluster][kEach];
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) c[e] = 0;
-        for (int r = 0; r < cluster; ++r) {
-          const uint32_t rc = cluster_address(&S.count[threadIdx.x * kEach], r);
+        for (int r = 0; r < kMaxCluster; ++r) {  // all on their way at once
+          const uint32_t rc = cluster_address(&S.count[threadIdx.x * kEach], min(r, cluster - 1));
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) c[e] += cluster_load32(rc + 4 * e);
+          for (int e = 0; e < kEach; ++e) got[r][e] = r < cluster ? cluster_load32(rc + 4 * e) : 0;
         }
-        if (threadIdx.x == 0) S.word[turn][0] = kBins;  // not reached
-        uint64_t left = block_before(S, (uint64_t)c[0] + c[1] + c[2] + c[3]);
+        uint64_t c[kEach], sum = 0, tokens = 0;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-          if (left < target && target <= left + c[e]) S.word[turn][0] = threadIdx.x * kEach + e;
+          c[e] = 0;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) c[e] += got[r][e];
+          if (!by_k) {
+            // mass at the bucket's near edge, less what the float arithmetic may add
+            tokens += (c[e] + 65535) >> 16;
+            const float near = exp2f(29.f - (threadIdx.x * kEach + e) / kSteps) * 0.999999f;
+            c[e] = __double2ull_rd((double)c[e] * (double)near);
+          }
+          sum += c[e];
+        }
+        const double want = ceil((double)p * (double)all_mass);
+        const uint64_t target = by_k ? (uint64_t)k : want > 1.0 ? (uint64_t)want : 1;
+        if (threadIdx.x == 0) S.word[turn][0] = kBins;  // not reached
+        uint64_t left = block_before(S, sum);
+        __syncthreads();
+        const uint64_t before = by_k ? 0 : block_before(S, tokens);  // tokens of nearer buckets, a few less
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          if (left < target && target <= left + c[e]) {
+            S.word[turn][0] = threadIdx.x * kEach + e;
+            S.word[turn][1] = before + tokens;
+          }
           left += c[e];
         }
       }
       cluster_barrier();
       const int bin = (int)word(S, turn, 0, 0);
       // the bucket's far edge, and what the bucketing rounds
-      if (bin < kBins)
-        reach = by_k ? (bin + 1) * ((float)kRange / kBins) * 1.00001f
-                     : ((bin + 1) * (1.f / kSteps) * 1.00001f) / W.log2_t;
+      if (bin < kBins && by_k) reach = (bin + 1) * ((float)kRange / kBins) * 1.00001f;
+      if (bin < kBins && !by_k) {
+        reach = ((bin + 1) * (1.f / kSteps) * 1.00001f) / W.log2_t;
+        if (word(S, turn, 1, 0) > kList - kList / 16) border_bin = bin;
+      }
     }
     // (with top-k, only its tokens may be dropped by min-p afterwards)
-    if (floor_w > 0.0 && !by_k) reach = fminf(reach, temperature * (0.01f - logf((float)floor_w)));
+    if (floor_w > 0.0 && !by_k) {
+      const float least = temperature * (0.01f - logf((float)floor_w));
+      if (least < reach) {
+        reach = least;
+        border_bin = -1;
+      }
+    }
     // the first CTA's go straight into its list, another's together
-#pragma unroll 2
+    uint64_t nearer = 0;
+    if (threadIdx.x == 0) S.local_n = 0;
+    __syncthreads();
+#pragma unroll 1
     for (int i = seg_lo + 4 * lane; i < seg_hi; i += 128) {
       const float4 v = *reinterpret_cast<const float4*>(z + i);
       const float x[4] = {v.x, v.y, v.z, v.w};
       if (!(W.zmax - fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) <= reach)) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (x[e] > -INFINITY && W.zmax - x[e] <= reach) {
-          if (rank == 0) {
-            const uint32_t at = atomicAdd(&S.list_n, 1u);
-            if (at < kList) S.list[at] = place(x[e], base + i + e);
-          } else {
-            const uint32_t at = atomicAdd(&S.local_n, 1u);
-            if (at < kLocal) S.local[at] = place(x[e], base + i + e);
-          }
+      for (int e = 0; e < 4; ++e) {
+        bool in = x[e] > -INFINITY && W.zmax - x[e] <= reach;
+        if (border_bin >= 0 && in) {
+          const float at = fmaxf(-W.log2_weight(x[e]), 0.f) * kSteps;
+          in = at >= (float)(border_bin - 1) && at < (float)(border_bin + 1);
+          if (at < (float)(border_bin - 1)) nearer += W.mass(x[e]);
         }
+        if (!in) continue;
+        const uint32_t at = atomicAdd(rank == 0 ? &S.list_n : &S.local_n, 1u);
+        if (rank == 0 && at < kList) S.list[at] = place(x[e], base + i + e);
+        if (rank != 0 && at < kLocal) S.local[at] = place(x[e], base + i + e);
+      }
+    }
+    if (border_bin >= 0) {
+      uint64_t same = 0;
+      block_join<false>(S, &nearer, &same);
+      turn ^= 1;
+      if (threadIdx.x == 0) S.word[turn][0] = nearer;
     }
     if (rank != 0) {
       __syncthreads();
@@ -651,19 +823,36 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
     }
     cluster_barrier();
     const uint32_t listed = cluster_load32(cluster_address(&S.list_n, 0));
-    cluster_arrive();  // this CTA has read the number
-    if (listed <= kList) {
+    if (border_bin < 0 && listed <= kList) {
+      cluster_arrive();  // this CTA has read the number
       if (rank == 0) {
-        if (listed <= 32 * kEach) {
-          if (warp == 0) finish<false>(S, A, b, W, f, (int)listed, all_mass);
-        } else {
-          finish<true>(S, A, b, W, f, (int)listed, all_mass);
-        }
+        if (listed <= kFew)
+          finish_few(S, A, b, W, f, (int)listed, all_mass);
+        else
+          finish_many(S, A, b, W, f, (int)listed, all_mass);
       }
       cluster_wait();
       return;
     }
-    cluster_wait();
+    if (border_bin >= 0 && listed <= kList) {
+      // the border among the listed ones, if it is among them
+      nearer = warp_sum64(words(S, turn, 0, cluster, 0));
+      turn ^= 1;
+      if (rank == 0) {
+        uint64_t in = 0, same = 0, last = kAll;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < (int)listed; i += kSampThreads) in += W.mass(logit_of(S.list[i]));
+        block_join<false>(S, &in, &same);
+        const double want = ceil((double)p * (double)all_mass);
+        const uint64_t target = want > 1.0 ? (uint64_t)want : (uint64_t)1;
+        if (nearer < target && target - nearer <= in)
+          last = select(S, W, (int)listed, true, target - nearer, kAll);
+        if (threadIdx.x == 0) S.word[turn][0] = last;
+      }
+      cluster_barrier();
+      upto = word(S, turn, 0, 0);
+      known = upto != kAll;
+    }
   }
 
   // The longer way.  Its buckets: the distance from zmax in steps of `range` /
@@ -671,7 +860,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   // one.  The distance rounds, the product rounds and the cut keeps the order,
   // so bins are ordered.
   float range = 0.f;
-  if (by_k || by_p) {
+  if (!known && (by_k || by_p)) {
     uint64_t low = kAll, same;
 #pragma unroll 2
     for (int i = seg_lo + lane; i < seg_hi; i += 32)
@@ -685,15 +874,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   const float bins_per = range > 0.f ? kBins / range : 0.f;
   const int n32 = (n + 31) & ~31;
 
-  // What is kept: tokens up to place `upto`, of weight floor_w at least.
-  uint64_t upto = kAll, sum = 0, before = 0, mine = 0, kept = 0;
+  uint64_t sum = 0, before = 0, mine = 0, kept = 0;
   // 0: top-k's border; 1: the mass of what it keeps, and top-p's border;
   // 2: the kept mass; 3: as 2, of the tokens of one logit (a tie at a border)
   float tie = 0.f;
   uint64_t target = 0;
   bool tied = false, tied_mass = false;
 #pragma unroll 1
-  for (int phase = 0; phase < 3;) {
+  for (int phase = known ? 2 : 0; phase < 3;) {
     if (phase == 0 && !tied && !by_k) {
       phase = 1;
       continue;
@@ -776,10 +964,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
         if (phase == 2) {
           if (here && threadIdx.x == 0) {
             const int at = S.found;
-            const double t = ((double)z[at] - (double)W.zmax) * W.inv_t;
-            A.tok[b] = base + at;
-            if (A.logprob) A.logprob[b] = (float)(t - log((double)sum / kOne));
-            if (A.kept) A.kept[b] = (int)kept;
+            answer(A, b, W, (uint32_t)(base + at), z[at], sum, (int)kept);
           }
           break;
         }
