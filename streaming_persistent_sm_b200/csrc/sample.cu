@@ -99,6 +99,7 @@ __device__ __forceinline__ double exp_neg(double t) {
 
 // 2^-kTail: weights below it are computed in 32 bits.
 constexpr float kTail = 14.f;
+constexpr float kFar = 24.f;  // see tail_mass
 
 struct Weigh {  // weights of a row's tokens
   float zmax, log2_t, log2_t_rest;  // log2(e) / T and what its float leaves
@@ -109,18 +110,21 @@ struct Weigh {  // weights of a row's tokens
   // log2 of the weight, to 2^-20 or so: enough to choose a way
   __device__ __forceinline__ float log2_weight(float z) const { return (z - zmax) * log2_t; }
   __device__ __forceinline__ uint64_t heavy_mass(float z) const { return __double2ull_rn(weight(z) * kOne); }
-  // The mass of a token of log2_weight t < -kTail.  The exponent is carried with
-  // its rounding errors (of the distance and of the product) and split into a
-  // whole number and a rest below 1/2, so the error is ex2's, 2^-22.
+  // The mass of a token of log2_weight t < -kTail.  Down to 2^-kFar the exponent
+  // is carried with its rounding errors (of the distance and of the product) and
+  // split into a whole number and a rest below 1/2, so the error is ex2's, 2^-22.
+  // Below, t's own rounding (2^-19 of the weight) no longer counts.
   __device__ __forceinline__ uint32_t tail_mass(float z, float t) const {
-    if (!(t > -48.f)) return 0;
-    const float d = z - zmax, back = d + zmax;
-    const float lost = (z - back) + (zmax - (back - d));  // z - zmax - d
-    const float n = rintf(t);
-    const float rest = (t - n) + fmaf(d, log2_t, -t) + fmaf(d, log2_t_rest, lost * log2_t);
-    float m;
+    float rest = t + 45.f, scale = 1.f, m;
+    if (!(t < -kFar)) {
+      const float d = z - zmax, back = d + zmax;
+      const float lost = (z - back) + (zmax - (back - d));  // z - zmax - d
+      const float n = rintf(t);
+      rest = (t - n) + fmaf(d, log2_t, -t) + fmaf(d, log2_t_rest, lost * log2_t);
+      scale = __int_as_float((int)n + (45 + 127) << 23);
+    }
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(m) : "f"(rest));
-    return __float2uint_rn(m * __int_as_float((int)n + (45 + 127) << 23));
+    return __float2uint_rn(m * scale);
   }
   __device__ __forceinline__ uint64_t mass(float z) const {
     const float t = log2_weight(z);
@@ -148,7 +152,7 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v) {  // inclusive
 }
 
 // Shared memory of a CTA, the slice's logits behind it.
-constexpr int kLocal = kBins / 2;  // candidates that a CTA other than the first can send
+constexpr int kLocalBits = 10, kLocal = 1 << kLocalBits;
 struct SampleShared {
   union {
     uint64_t mass[kBins];
@@ -156,12 +160,12 @@ struct SampleShared {
   };
   union {
     uint32_t count[kBins];
-    uint64_t local[kLocal];  // the bins are read before the candidates are collected
+    uint64_t local[kLocal];  // the first CTA's, once the buckets are read
   };
   uint64_t warp_a[kSampWarps], warp_b[kSampWarps];
   uint64_t word[2][4];  // what this CTA tells the others, in turn
   uint32_t part[3][kSampWarps];
-  uint32_t list_n, local_n, local_at;
+  uint32_t list_n, local_n, local_at;  // entries of the list, of `local` (of the list, elsewhere than first)
   int found;
 };
 static_assert(sizeof(SampleShared) % 16 == 0, "the slice behind it is aligned");
@@ -234,62 +238,6 @@ __device__ __forceinline__ uint64_t block_before(SampleShared& S, uint64_t v) {
 }
 
 constexpr int kEach = kList / kSampThreads;  // entries of the list that a thread holds
-static_assert(kEach == 4, "sort_each holds four");
-
-// Sorts `size` entries (a power of two, 128 or more), four in each of the first
-// size / 4 threads, ascending, as a bitonic network: partners are in the thread,
-// in the warp (shuffles), or, above 128 entries, in another warp (through the
-// list).  Called by whole CTAs where size > 128.
-__device__ __forceinline__ void sort_each(SampleShared& S, uint64_t (&v)[kEach], int size) {
-  const int i0 = kEach * threadIdx.x;
-#pragma unroll 1
-  for (int s = 2; s <= size; s *= 2)
-#pragma unroll 1
-    for (int j = s / 2; j > 0; j /= 2) {
-      if (j >= 32 * kEach) {
-        __syncthreads();
-        if (i0 < size) {
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) S.list[i0 + e] = v[e];
-        }
-        __syncthreads();
-        if (i0 < size) {
-          const bool low = ((i0 & j) == 0) == ((i0 & s) == 0);
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            const uint64_t other = S.list[(i0 ^ j) + e];
-            v[e] = low ? min(v[e], other) : max(v[e], other);
-          }
-        }
-      } else if (j >= kEach) {
-        const bool low = ((i0 & j) == 0) == ((i0 & s) == 0);
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-          const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, v[e], j / kEach);
-          v[e] = low ? min(v[e], other) : max(v[e], other);
-        }
-      } else {
-        auto order = [&](int x, int y) {  // entries x < y of the thread
-          const bool up = ((i0 + x) & s) == 0;
-          const uint64_t a = min(v[x], v[y]), c = max(v[x], v[y]);
-          v[x] = up ? a : c;
-          v[y] = up ? c : a;
-        };
-        if (j == 2) {
-          order(0, 2);
-          order(1, 3);
-        } else {
-          order(0, 1);
-          order(2, 3);
-        }
-      }
-    }
-}
-__device__ __forceinline__ int sort_size(int n) {
-  int size = 32 * kEach;
-  while (size < n) size *= 2;
-  return size;
-}
 
 struct Filters {
   int k;           // top-k's number, where it is on
@@ -380,29 +328,30 @@ __device__ __forceinline__ void finish_few(SampleShared& S, const SampleArgs& A,
   draw_few(S, A, b, W, f.u, n);
 }
 
-// Among the n tokens of the list (kFew < n <= kList; whole CTAs) that `upto`
-// does not leave out: the place of the last one of the shortest beginning whose
-// number (or mass) reaches `target`, which all of them together do.  They fall
-// into 1024 bins by the bits of their logits; the ones of the border's bin are
-// compared with one another.
-__device__ __forceinline__ uint64_t select(SampleShared& S, const Weigh& W, int n, bool by_mass, uint64_t target,
-                                           uint64_t upto) {
+// Among the n <= kList keys of the list (whole CTAs) up to `upto`: the last one
+// of the shortest beginning, in ascending order, whose number (or mass) reaches
+// `target`, which all of them together do.  Keys are places, or ids with the
+// rank bits' complement below them (by_id).  They fall into bins by their high
+// word; the ones of the border's bin are compared with one another.
+__device__ __forceinline__ uint64_t select(SampleShared& S, const Weigh& W, int n, bool by_mass, bool by_id,
+                                           uint64_t target, uint64_t upto) {
   uint64_t least = kAll, most = kAll;
 #pragma unroll 1
   for (int i = threadIdx.x; i < n; i += kSampThreads) {
-    const uint32_t r = ~(uint32_t)(S.list[i] >> 32);
-    least = min(least, (uint64_t)r);
-    most = min(most, (uint64_t)~r);
+    const uint64_t key = S.list[i];
+    least = min(least, key);
+    if (key <= upto) most = min(most, ~key);
   }
   block_join<true>(S, &least, &most);
-  const uint32_t lo = (uint32_t)least, hi = ~(uint32_t)most;
+  const uint32_t lo = (uint32_t)(least >> 32), span = (uint32_t)(~most >> 32) - lo;
+  const int shift = max(0, 32 - __clz(span) - kLocalBits);
   for (int i = threadIdx.x; i < kLocal; i += kSampThreads) S.local[i] = 0;
   if (threadIdx.x == 0) S.local_n = 0;
   __syncthreads();
-  auto bin_of = [&](uint64_t key) {
-    return (int)((uint64_t)(hi - ~(uint32_t)(key >> 32)) * kLocal / ((uint64_t)(hi - lo) + 1));
+  auto bin_of = [&](uint64_t key) { return (int)(((uint32_t)(key >> 32) - lo) >> shift); };
+  auto worth = [&](uint64_t key) {
+    return by_mass ? W.mass(from_rank(~(uint32_t)(by_id ? key : key >> 32))) : (uint64_t)1;
   };
-  auto worth = [&](uint64_t key) { return by_mass ? W.mass(logit_of(key)) : (uint64_t)1; };
 #pragma unroll 1
   for (int i = threadIdx.x; i < n; i += kSampThreads) {
     const uint64_t key = S.list[i];
@@ -411,7 +360,7 @@ __device__ __forceinline__ uint64_t select(SampleShared& S, const Weigh& W, int 
   }
   __syncthreads();
   {
-    static_assert(kLocal == 2 * kSampThreads, "two bins a thread");
+    static_assert(kLocal == 2 * kSampThreads && kLocal == 1 << kLocalBits, "two bins a thread");
     const uint64_t v0 = S.local[2 * threadIdx.x], v1 = S.local[2 * threadIdx.x + 1];
     const uint64_t left = block_before(S, v0 + v1);
     if (left < target && target <= left + v0 + v1) {
@@ -423,7 +372,7 @@ __device__ __forceinline__ uint64_t select(SampleShared& S, const Weigh& W, int 
   __syncthreads();
   const int bin = S.found;
   target -= S.warp_b[0];
-  // its tokens, together (as many as there is room for)
+  // its keys, together (as many as there is room for)
 #pragma unroll 1
   for (int i = threadIdx.x; i < n; i += kSampThreads) {
     const uint64_t key = S.list[i];
@@ -470,7 +419,7 @@ __device__ __forceinline__ void finish_many(SampleShared& S, const SampleArgs& A
       target = want > 1.0 ? (uint64_t)want : (uint64_t)1;
       if (target > in) continue;  // all of the list (min-p ends it)
     }
-    if (by_mass || target < (uint64_t)n) upto = select(S, W, n, by_mass, target, upto);
+    if (by_mass || target < (uint64_t)n) upto = select(S, W, n, by_mass, false, target, upto);
   }
   // the kept ones together
   __syncthreads();
@@ -507,24 +456,9 @@ __device__ __forceinline__ void finish_many(SampleShared& S, const SampleArgs& A
       S.list[at] = key[e] << 32 | key[e] >> 32;
     }
   __syncthreads();
-  uint64_t sum = 0, w[kEach];
-  const int i0 = kEach * threadIdx.x;
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) key[e] = i0 + e < (int)kept ? S.list[i0 + e] : kAll;
-  sort_each(S, key, sort_size((int)kept));
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    w[e] = i0 + e < (int)kept ? W.mass(from_rank(~(uint32_t)key[e])) : 0;
-    sum += w[e];
-  }
-  uint64_t left = block_before(S, sum);
   const uint64_t want = min((uint64_t)(f.u * (double)mass), mass - 1);
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    if (left <= want && want < left + w[e])  // in one thread
-      answer(A, b, W, (uint32_t)(key[e] >> 32), from_rank(~(uint32_t)key[e]), mass, (int)kept);
-    left += w[e];
-  }
+  const uint64_t drawn = select(S, W, (int)kept, true, true, want + 1, kAll);
+  if (threadIdx.x == 0) answer(A, b, W, (uint32_t)(drawn >> 32), from_rank(~(uint32_t)drawn), mass, (int)kept);
 }
 
 template <typename T>
@@ -540,6 +474,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   const float temperature = A.temperature ? A.temperature[b] : 1.f, u_part = A.uniform[b];
   const float p = A.top_p ? A.top_p[b] : 1.f, mp = A.min_p ? A.min_p[b] : 0.f;
   const int k = A.top_k ? A.top_k[b] : 0;
+
+  for (int i = threadIdx.x; i < kBins; i += kSampThreads) S.count[i] = 0;
+  if (threadIdx.x == 0) S.list_n = 0;
 
   // read the slice, padded with masked tokens to whole vectors of all lanes
   const int padded = (n + 127) & ~127;
@@ -581,8 +518,6 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
       S.part[1][warp] = c;
       S.part[2][warp] = w;
     }
-    for (int i = threadIdx.x; i < kBins; i += kSampThreads) S.count[i] = 0;
-    if (threadIdx.x == 0) S.list_n = S.local_n = 0;
     __syncthreads();
     const bool on = lane < kSampWarps;
     const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, on ? S.part[0][lane] : 0u),
@@ -638,10 +573,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   const bool filtered = by_k || by_p || floor_w > 0.0;
 
   // The mass of all tokens: what a row without filters draws from, and top-p
-  // alone is measured by.  For the latter, tokens fall into buckets of 1/48 of
-  // their weights' log2; a bucket sums up 2^16 times what its tokens weigh
-  // against its near edge, rounded down (1 - x ln 2 <= 2^-x).
-  constexpr float kSteps = 48.f;
+  // alone is measured by.  For the latter, tokens of 2^-kFar and more fall into
+  // buckets of 1/80 of their weights' log2; a bucket sums up 2^13 times what its
+  // tokens weigh against its near edge, rounded down (1 - x ln 2 <= 2^-x); 2^18
+  // tokens fit 32 bits.
+  constexpr float kSteps = 80.f;
+  static_assert(kFar * kSteps < kBins, "a bucket for every token");
   uint64_t all_mass = 0;
   if (!filtered || (by_p && !by_k)) {
     uint64_t v = 0;
@@ -656,9 +593,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
           v += W.tail_mass(x[e], t);
         else if (x[e] > -INFINITY)
           v += W.heavy_mass(x[e]);
-        if (filtered) {
+        if (filtered && !(t < -kFar)) {
           const float at = fmaxf(-t, 0.f) * kSteps, edge = floorf(at);  // a NaN is 0
-          if (at < (float)kBins) atomicAdd(&S.count[(int)edge], (uint32_t)(65536.f - (at - edge) * (45426.1f / kSteps)));
+          atomicAdd(&S.count[(int)edge], (uint32_t)(8192.f - (at - edge) * (5678.27f / kSteps)));
         }
       }
     }
@@ -723,52 +660,73 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
         }
         cluster_barrier();
       }
-      // rank 0 sums the CTAs' buckets and finds the one that reaches the target
-      turn ^= 1;
-      if (rank == 0) {
-        uint32_t got[kMaxCluster][kEach];
+      // each CTA sums up its share of the buckets over the cluster; the share
+      // that reaches the target is then read by all
+      const int share = kBins / cluster + (kBins % cluster != 0);  // >= 256
+      const int first = rank * share, mine_n = max(0, min(share, kBins - first));
+      const double want = ceil((double)p * (double)all_mass);
+      const uint64_t target = by_k ? (uint64_t)k : want > 1.0 ? (uint64_t)want : 1;
+      auto worth = [&](int bin, uint64_t c) {  // mass at the near edge, less what the float arithmetic may add
+        return by_k ? c : __double2ull_rd((double)c * (double)(exp2f(32.f - bin / kSteps) * 0.999999f));
+      };
+      uint64_t sum = 0, tokens = 0;
+#pragma unroll 1
+      for (int i = threadIdx.x; i < mine_n; i += kSampThreads) {
+        uint32_t got[kMaxCluster];
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {  // all on their way at once
-          const uint32_t rc = cluster_address(&S.count[threadIdx.x * kEach], min(r, cluster - 1));
+        for (int r = 0; r < kMaxCluster; ++r)  // all on their way at once
+          got[r] = r < cluster ? cluster_load32(cluster_address(&S.count[first + i], r)) : 0;
+        uint32_t c = 0;
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) got[r][e] = r < cluster ? cluster_load32(rc + 4 * e) : 0;
-        }
-        uint64_t c[kEach], sum = 0, tokens = 0;
+        for (int r = 0; r < kMaxCluster; ++r) c += got[r];
+        S.count[first + i] = c;  // this share of this CTA's buckets is read by itself alone
+        tokens += (c + 8191) >> 13;
+        sum += worth(first + i, c);
+      }
+      block_join<false>(S, &sum, &tokens);
+      meet(S, turn, sum, tokens);
+      sum = words(S, turn, 0, cluster, 0);
+      tokens = words(S, turn, 1, cluster, 0);
+      const uint64_t upto_rank = warp_scan64(sum), tokens_upto = warp_scan64(tokens);
+      const uint32_t over = __ballot_sync(0xFFFFFFFFu, lane < cluster && upto_rank >= target);
+      int bin = kBins;  // not reached
+      uint64_t near = 0;  // tokens up to the bucket (top-p), roughly
+      if (over) {
+        const int owner = __ffs(over) - 1;
+        uint64_t left = __shfl_sync(0xFFFFFFFFu, upto_rank - sum, owner);
+        near = __shfl_sync(0xFFFFFFFFu, tokens_upto - tokens, owner);
+        const int at0 = owner * share, q = (share + kSampThreads - 1) / kSampThreads;
+        uint64_t c[kEach], all = 0, in_bins = 0;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-          c[e] = 0;
-#pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r) c[e] += got[r][e];
-          if (!by_k) {
-            // mass at the bucket's near edge, less what the float arithmetic may add
-            tokens += (c[e] + 65535) >> 16;
-            const float near = exp2f(29.f - (threadIdx.x * kEach + e) / kSteps) * 0.999999f;
-            c[e] = __double2ull_rd((double)c[e] * (double)near);
-          }
-          sum += c[e];
+          const int i = at0 + threadIdx.x * q + e;
+          const bool in = e < q && i < min(at0 + share, kBins);
+          const uint32_t n_in = in ? cluster_load32(cluster_address(&S.count[i], owner)) : 0;
+          c[e] = worth(i, n_in);
+          all += c[e];
+          in_bins += (n_in + 8191) >> 13;
         }
-        const double want = ceil((double)p * (double)all_mass);
-        const uint64_t target = by_k ? (uint64_t)k : want > 1.0 ? (uint64_t)want : 1;
-        if (threadIdx.x == 0) S.word[turn][0] = kBins;  // not reached
-        uint64_t left = block_before(S, sum);
-        __syncthreads();
-        const uint64_t before = by_k ? 0 : block_before(S, tokens);  // tokens of nearer buckets, a few less
+        if (threadIdx.x == 0) S.found = kBins;
+        left += block_before(S, all);
+        __syncthreads();  // warp_a is read
+        const uint64_t nearer = block_before(S, in_bins) + in_bins;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
           if (left < target && target <= left + c[e]) {
-            S.word[turn][0] = threadIdx.x * kEach + e;
-            S.word[turn][1] = before + tokens;
+            S.found = at0 + threadIdx.x * q + e;
+            S.warp_b[0] = nearer;
           }
           left += c[e];
         }
+        __syncthreads();
+        bin = S.found;
+        near += S.warp_b[0];
       }
-      cluster_barrier();
-      const int bin = (int)word(S, turn, 0, 0);
       // the bucket's far edge, and what the bucketing rounds
       if (bin < kBins && by_k) reach = (bin + 1) * ((float)kRange / kBins) * 1.00001f;
       if (bin < kBins && !by_k) {
         reach = ((bin + 1) * (1.f / kSteps) * 1.00001f) / W.log2_t;
-        if (word(S, turn, 1, 0) > kList - kList / 16) border_bin = bin;
+        if (near > kList - kList / 16) border_bin = bin;
       }
     }
     // (with top-k, only its tokens may be dropped by min-p afterwards)
@@ -798,8 +756,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
         }
         if (!in) continue;
         const uint32_t at = atomicAdd(rank == 0 ? &S.list_n : &S.local_n, 1u);
-        if (rank == 0 && at < kList) S.list[at] = place(x[e], base + i + e);
-        if (rank != 0 && at < kLocal) S.local[at] = place(x[e], base + i + e);
+        if (at < kList) S.list[at] = place(x[e], base + i + e);
       }
     }
     if (border_bin >= 0) {
@@ -811,14 +768,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
     if (rank != 0) {
       __syncthreads();
       const uint32_t n_local = S.local_n;
-      if (n_local) {  // more than can be sent: as many as the list does not hold
-        if (threadIdx.x == 0)
-          S.local_at = cluster_add32(cluster_address(&S.list_n, 0), n_local <= kLocal ? n_local : kList + 1);
+      if (n_local) {
+        if (threadIdx.x == 0) S.local_at = cluster_add32(cluster_address(&S.list_n, 0), n_local);
         __syncthreads();
         const uint32_t to = cluster_address(S.list, 0), at = S.local_at;
-        if (n_local <= kLocal)
-          for (uint32_t i = threadIdx.x; i < n_local; i += kSampThreads)
-            if (at + i < kList) cluster_store64(to + 8 * (at + i), S.local[i]);
+        for (uint32_t i = threadIdx.x; i < n_local && at + i < kList; i += kSampThreads)
+          cluster_store64(to + 8 * (at + i), S.list[i]);
       }
     }
     cluster_barrier();
@@ -846,7 +801,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
         const double want = ceil((double)p * (double)all_mass);
         const uint64_t target = want > 1.0 ? (uint64_t)want : (uint64_t)1;
         if (nearer < target && target - nearer <= in)
-          last = select(S, W, (int)listed, true, target - nearer, kAll);
+          last = select(S, W, (int)listed, true, false, target - nearer, kAll);
         if (threadIdx.x == 0) S.word[turn][0] = last;
       }
       cluster_barrier();
@@ -1079,24 +1034,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
         cluster_barrier();
         turn ^= 1;
         if (rank == 0) {
-          uint64_t key[kEach], v[kEach], sum = 0;
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            const int i = kEach * threadIdx.x + e;
-            key[e] = i < (int)tokens ? S.list[i] : kAll;
-          }
-          sort_each(S, key, sort_size((int)tokens));
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            v[e] = key[e] == kAll ? 0 : by_mass ? W.mass(from_rank(~(uint32_t)(key[e] >> 32))) : 1;
-            sum += v[e];
-          }
-          uint64_t left = block_before(S, sum);
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            if (left < target && target <= left + v[e]) S.word[turn][0] = key[e];
-            left += v[e];
-          }
+          const uint64_t last = select(S, W, (int)tokens, by_mass, false, target, kAll);
+          if (threadIdx.x == 0) S.word[turn][0] = last;
         }
         cluster_barrier();
         upto = word(S, turn, 0, 0);
