@@ -1,4 +1,5 @@
-"""Build the in-tree shared library ``libwpk.so`` (sm_100a) with nvcc.
+"""Build the in-tree shared library ``libwpk.so`` (sm_100a) with nvcc, and the
+module ``_wpk_torch.so`` that calls its operators on torch tensors.
 
 Usage: ``python -m streaming_persistent_sm_b200.build [--verbose]``.  The
 library is written next to this file so that it travels with the source tree.
@@ -14,6 +15,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwpk.so")
+TORCH_LIB = os.path.join(HERE, "_wpk_torch.so")
 SOURCES = ["graph.cpp", "planner.cpp", "runtime.cu", "capi.cu", "noalloc.cu", "debug_gemm.cu", "kv4.cu",
            "kv4_attention.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -55,7 +57,33 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(LIB + ".tmp", LIB)
+    build_torch_ops(verbose)
     return LIB
+
+
+def build_torch_ops(verbose: bool = False) -> str:
+    """The torch module (host code only), linked to the libwpk.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    torch_libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           "-DTORCH_EXTENSION_NAME=_wpk_torch", *[a for i in includes for a in ("-isystem", i)],
+           os.path.join(CSRC, "torch_ops.cpp"), "-o", TORCH_LIB + ".tmp", "-L", HERE, "-l:libwpk.so", "-L", torch_libs,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on torch_ops.cpp")
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    return TORCH_LIB
 
 
 if __name__ == "__main__":

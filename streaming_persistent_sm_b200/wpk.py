@@ -386,55 +386,34 @@ def wpk_sample(logits_dev: int, dtype: int, batch: int, vocab: int, row_stride: 
 
 
 # ------------------------------------------------- operators on torch tensors --
-_DTYPES = {}  # torch dtype -> WPK_*, filled with the first use of torch
+_ops_module = None
 
 
-def _torch():
-    import torch
+def _ops():
+    """The module that calls the operators on torch tensors (raises if it was not built)."""
+    global _ops_module
+    if _ops_module is None:
+        import importlib.util
 
-    if not _DTYPES:
-        _DTYPES.update({torch.float32: WPK_F32, torch.bfloat16: WPK_BF16, torch.float16: WPK_F16})
-    return torch
+        import torch  # noqa: F401  (its libraries, before the module's)
 
-
-class _on:
-    """The device of a call's tensors made current for it, and its stream there."""
-
-    __slots__ = ("torch", "index", "before", "stream")
-
-    def __init__(self, torch, device):
-        self.torch, self.index = torch, device.index
-
-    def __enter__(self):
-        cuda = self.torch.cuda
-        self.before = cuda.current_device()
-        if self.before != self.index:
-            cuda.set_device(self.index)
-        self.stream = cuda.current_stream().cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            self.torch.cuda.set_device(self.before)
-
-
-def _bad(msg: str):
-    raise WpkError(WPK_ERR_INVALID_ARG, msg)
-
-
-def _vector(x, name: str, dtype, n: int, device) -> int:
-    """Address of a contiguous vector of n elements on the device (0 for None)."""
-    if x is None:
-        return 0
-    if x.dtype != dtype or x.device != device or x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
-        _bad(f"{name} must be a contiguous {dtype} tensor [{n}] on {device}")
-    return x.data_ptr()
+        path = os.path.join(_HERE, "_wpk_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m streaming_persistent_sm_b200.build`")
+        load_library()
+        spec = importlib.util.spec_from_file_location("_wpk_torch", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_error(WpkError)
+        _ops_module = m
+    return _ops_module
 
 
 def rope_table(positions: int, head_dim: int, theta: float = 10000.0, device="cuda"):
     """(cos, sin) of p * theta^(-2 i / head_dim) for the positions p < `positions`, fp32
     [positions][head_dim / 2][2], the angles in 64 bits: the rotation of the step programs."""
-    torch = _torch()
+    import torch
+
     inv = float(theta) ** (-2.0 * torch.arange(head_dim // 2, dtype=torch.float64, device=device) / head_dim)
     a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
     return torch.stack([a.cos(), a.sin()], dim=-1).float().contiguous()
@@ -450,78 +429,34 @@ class KV4Cache:
     ``indptr`` (int32 [batch + 1]).  Calls run on the current stream of the cache's device."""
 
     def __init__(self, n_blocks: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64, device=None):
-        torch = _torch()
+        import torch
+
         device = torch.device("cuda" if device is None else device)
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         if n_blocks <= 0 or n_kv_heads <= 0:
-            _bad("n_blocks and n_kv_heads must be positive")
+            raise WpkError(WPK_ERR_INVALID_ARG, "n_blocks and n_kv_heads must be positive")
         self.n_blocks, self.n_kv_heads, self.head_dim, self.page_tokens = n_blocks, n_kv_heads, head_dim, page_tokens
-        self.device = device
         # zeros: rows that were never appended read as zeros
         self.pages = torch.zeros((n_blocks, n_kv_heads, wpk_kv4_page_bytes(head_dim, page_tokens)), dtype=torch.uint8,
                                  device=device)
-
-    def _call(self, torch, pos, table, indptr, rope):
-        """The call's cache struct and the addresses of its position, indptr and rope tensors."""
-        dev = self.device
-        if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or not table.is_contiguous():
-            _bad(f"block_table must be a contiguous int32 tensor [batch][max_blocks] on {dev}")
-        batch, blocks = table.shape
-        pos = _vector(pos, "pos", torch.int32, batch, dev)
-        indptr = _vector(indptr, "indptr", torch.int32, batch + 1, dev)
-        n_rope = 0
-        if rope is not None:
-            if (rope.dtype != torch.float32 or rope.device != dev or rope.dim() != 3 or not rope.is_contiguous()
-                    or rope.shape[1] != self.head_dim // 2 or rope.shape[2] != 2):
-                _bad(f"rope must be a contiguous fp32 tensor [positions][{self.head_dim // 2}][2] on {dev}")
-            n_rope, rope = rope.shape[0], rope.data_ptr()
-        c = wpk_kv4_cache(self.pages.data_ptr(), table.data_ptr(), self.n_blocks, batch, blocks, self.n_kv_heads,
-                          self.head_dim, self.page_tokens)
-        return c, pos, indptr, rope or 0, n_rope
-
-    def _rows(self, x, name: str, total: int, heads: int):
-        """Address and strides of a tensor of rows, and its element type."""
-        if x.dtype not in _DTYPES or x.device != self.device or x.shape != (total, heads, self.head_dim):
-            _bad(f"{name} must be a float32, bfloat16 or float16 tensor [{total}][{heads}][{self.head_dim}] on "
-                 f"{self.device}")
-        s = x.stride()
-        if s[2] != 1:
-            _bad(f"{name} must be contiguous in its last dimension")
-        # the stride of a dimension of one element says nothing
-        return x.data_ptr(), (s[0] if total > 1 else 0, s[1] if heads > 1 else 0), _DTYPES[x.dtype]
+        self.device = self.pages.device
+        self._calls = _ops().Kv4(self.pages, n_kv_heads, head_dim, page_tokens)
 
     def append(self, k, v, pos, block_table, indptr=None, rope=None):
         """Quantise the rows of k (rotated to their positions by ``rope``, see rope_table) and v
         [total][n_kv_heads][head_dim] into the pages."""
-        torch = _torch()
-        total = k.shape[0]
-        c, p, i, r, n_rope = self._call(torch, pos, block_table, indptr, rope)
-        kp, ks, kt = self._rows(k, "k", total, self.n_kv_heads)
-        vp, vs, vt = self._rows(v, "v", total, self.n_kv_heads)
-        if kt != vt:
-            _bad("k and v must have one dtype")
-        if total == 0:
-            return
-        with _on(torch, self.device) as on:
-            wpk_kv4_append(c, p, i, total, kp, ks, vp, vs, kt, r, n_rope, on.stream)
+        self._calls.append(k, v, pos, block_table, indptr, rope)
 
     def read(self, pos, block_table, total: int, indptr=None, dtype=None):
         """The rows held for `total` tokens, counted as append counts them: k and v
         [total][n_kv_heads][head_dim] in ``dtype`` (bfloat16).  Rows that belong to no sequence of
         ``indptr`` are not written."""
-        torch = _torch()
-        dtype = dtype or torch.bfloat16
-        if dtype not in _DTYPES or total < 0:
-            _bad("dtype must be float32, bfloat16 or float16, and total >= 0")
-        c, p, i, _, _ = self._call(torch, pos, block_table, indptr, None)
-        k = torch.empty((total, self.n_kv_heads, self.head_dim), dtype=dtype, device=self.device)
-        v = torch.empty_like(k)
-        if total:
-            with _on(torch, self.device) as on:
-                wpk_kv4_read(c, p, i, total, k.data_ptr(), k.stride()[:2], v.data_ptr(), v.stride()[:2],
-                             _DTYPES[dtype], on.stream)
-        return k, v
+        if dtype is None:
+            import torch
+
+            dtype = torch.bfloat16
+        return self._calls.read(pos, block_table, total, indptr, dtype)
 
     def attention(self, q, pos, block_table, indptr=None, max_new: Optional[int] = None, rope=None, scale: float = 0.0,
                   out=None):
@@ -529,22 +464,7 @@ class KV4Cache:
         which hold the new tokens' keys and values already (append them first).  ``rope`` rotates q
         on the way.  ``max_new`` bounds the tokens of one sequence (default: total, or total / batch
         without ``indptr``); a close bound starts fewer thread blocks."""
-        torch = _torch()
-        if q.dim() != 3:
-            _bad("q must be [total][n_heads][head_dim]")
-        total, heads = q.shape[0], q.shape[1]
-        c, p, i, r, n_rope = self._call(torch, pos, block_table, indptr, rope)
-        qp, qs, qt = self._rows(q, "q", total, heads)
-        if out is None:
-            out = torch.empty((total, heads, self.head_dim), dtype=q.dtype, device=self.device)
-        elif out.dtype != q.dtype:
-            _bad("out must have q's dtype")
-        op, os_, _ = self._rows(out, "out", total, heads)
-        if total:
-            with _on(torch, self.device) as on:
-                wpk_kv4_attention(c, p, i, total, total if max_new is None else max_new, qp, qs, heads, qt, op, os_,
-                                  r, n_rope, scale, on.stream)
-        return out
+        return self._calls.attention(q, pos, block_table, indptr, max_new, rope, scale, out)
 
 
 def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, out_tok=None,
@@ -553,29 +473,11 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None
     uniform numbers (fp32 [batch] in [0, 1)); see wpk_sample.  temperature, top_p, min_p: fp32
     [batch]; top_k: int32 [batch]; None = off.  Returns the int32 tokens, and, where wanted, their
     log-probabilities (fp32) in the distribution drawn from and the numbers of tokens kept (int32)."""
-    torch = _torch()
-    if logits.dtype not in _DTYPES or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        _bad("logits must be a float32, bfloat16 or float16 tensor [batch][vocab], contiguous in its last dimension")
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
-    if dev.type != "cuda":
-        _bad("logits must be on a CUDA device")
-    B, V = logits.shape
-    if uniform is None:
-        _bad("uniform must be given")
-    args = [_vector(x, n, t, B, dev) for x, n, t in
-            ((uniform, "uniform", f32), (temperature, "temperature", f32), (top_k, "top_k", i32),
-             (top_p, "top_p", f32), (min_p, "min_p", f32))]
-    if out_tok is None:
-        out_tok = torch.empty(B, dtype=i32, device=dev)
-    op = _vector(out_tok, "out_tok", i32, B, dev)
-    logprob = torch.empty(B, dtype=f32, device=dev) if want_logprob else None
-    kept = torch.empty(B, dtype=i32, device=dev) if want_kept else None
-    if B:
-        with _on(torch, dev) as on:
-            wpk_sample(logits.data_ptr(), _DTYPES[logits.dtype], B, V, logits.stride(0), args[0], op, *args[1:],
-                       logprob.data_ptr() if want_logprob else 0, kept.data_ptr() if want_kept else 0, on.stream)
-    out = (out_tok,) + ((logprob,) if want_logprob else ()) + ((kept,) if want_kept else ())
-    return out if len(out) > 1 else out_tok
+    tok, logprob, kept = _ops().sample(logits, uniform, temperature, top_k, top_p, min_p, out_tok, want_logprob,
+                                       want_kept)
+    if not want_logprob and not want_kept:
+        return tok
+    return (tok,) + ((logprob,) if want_logprob else ()) + ((kept,) if want_kept else ())
 
 
 # ------------------------------------------------------------------ Engine --
