@@ -25,7 +25,6 @@
 // memory: one launch, no workspace, no atomics, so the result does not depend
 // on timing.  Each warp streams its pages through its own ring of shared-memory
 // stages with 16-byte asynchronous copies; nothing spins.
-#include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
 
@@ -38,25 +37,27 @@
 #include "op_util.cuh"
 #include "ptx.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace wpk {
 namespace {
 
 constexpr int kRows = 8;    // query rows of a CTA (the N of the P V product)
 constexpr int kKeys = 64;   // keys of a warp's step
+constexpr int kMaxSplit = 16;
 
-template <int HD>
+// A CTA of WARPS warps: 4, of which an SM holds four (three at head_dim 128), or
+// 12, one to an SM, where 16 CTAs a cluster would not fill the GPU otherwise.
+template <int HD, int WARPS>
 struct Geo {
-  static constexpr int kWarps = 8;
-  static constexpr int kStages = 3;
+  static constexpr int kPerSm = WARPS == 12 ? 1 : HD == 64 ? 4 : 3;
+  static constexpr int kStages = HD == 64 && WARPS == 12 ? 3 : 2;
   static constexpr int kRowBytes = HD / 2;
   static constexpr int kStageBytes = kKeys * (2 * kRowBytes + 8);  // K codes, V codes, K (s, z), V (s, z)
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
-  // after the keys: every warp's rows (O, then m, l and the sum of p z), then the CTA's
+  static constexpr int kWarpBytes = kStages * kStageBytes + kKeys * 16;  // and the step's scales as floats
+  static constexpr int kRing = WARPS * kWarpBytes;
+  // after the keys: every warp's rows (O, then m, l and the sum of p y), then the CTA's
   static constexpr int kWarpPart = kRows * (HD + 3);  // floats
   static constexpr int kCtaPart = kRows * (HD + 2);
-  static constexpr int kJoin = (kWarps * kWarpPart + kCtaPart) * 4;
+  static constexpr int kJoin = (WARPS * kWarpPart + kCtaPart) * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
@@ -112,18 +113,26 @@ __device__ __forceinline__ uint32_t centred_odd(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
+// What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's
+// codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
+// that the output's rounding is off, relative, of random values).  fp16: Q to 22
+// bits, V centred.  fp32: K centred and P to 22 bits too, and a step's own sums,
+// since the tensor pipe cuts off what its sums cannot hold.
+template <typename T>
+struct Keep {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value, kFp32 = std::is_same<T, float>::value;
+  static constexpr bool kQLow = !kBf16, kPLow = kFp32, kCentreK = kFp32, kCentreV = !kBf16, kOwnSums = kBf16 || kFp32;
+};
+
 // In a warp, lane = 4 g + t.  S's columns 2t and 2t + 1 of the n-th group of 8
 // keys are its keys t and 7 - t: with this order neither the K rows (8 at a
 // time) nor the V words (4 rows x 8 words) of a step meet in a bank.
-template <typename T, int HD>
-__global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
+template <typename T, int HD, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     kv4_attention_kernel(const Kv4Dev c, const T* __restrict__ q, T* __restrict__ out, const AttnArgs a) {
-  using G = Geo<HD>;
-  constexpr int WPL = HD / 32;          // words of a K row that a lane multiplies
-  // P keeps 22 bits (two products) for fp32 and fp16 tensors.  For bf16 ones its
-  // 11 bits are enough: they add 4e-4 to the output's own rounding of 1.7e-3
-  // (relative, of random values), but would double fp16's 2e-4.
-  constexpr bool kFull = !std::is_same<T, __nv_bfloat16>::value;
+  using G = Geo<HD, WARPS>;
+  using P = Keep<T>;
+  constexpr int WPL = HD / 32;  // words of a K row that a lane multiplies
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = blockIdx.x % a.split;
@@ -132,6 +141,23 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
   item /= a.row_blocks;
   const int head = item % c.n_kv, b = item / c.n_kv;
   if (b >= kv4_sequences(c)) return;  // as for every CTA of the cluster
+
+  // This warp's first step's keys, four runs of 16 inside a page each (one run of
+  // 64 where pages hold whole steps).  Lane i < runs keeps run i's place in the
+  // table from step to step.  The first page ids are asked for before it is known
+  // how many keys there are.
+  const int stride = a.split * WARPS, first = rank * WARPS + warp;
+  const bool whole = c.page_tokens % kKeys == 0;
+  const int32_t* table = c.table + (int64_t)b * c.max_blocks;
+  const int ahead = stride * kKeys, skip_slots = ahead / c.page_tokens, skip_rows = ahead % c.page_tokens;
+  int64_t key = (int64_t)first * kKeys + 16 * lane;
+  int slot = (int)(key / c.page_tokens), row = (int)(key % c.page_tokens);
+  auto ask = [&]() {  // the id of the page of the run
+    return lane < (whole ? 1 : 4) && slot < c.max_blocks ? table[slot] : -1;
+  };
+  int block = ask();
+
+  const int pos0 = c.pos[b];
   int q0, n_new;
   kv4_new(c, b, &q0, &n_new);
   const int64_t rows = (int64_t)min(n_new, a.max_new) * a.group;
@@ -139,16 +165,76 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
   if (r0 >= rows) return;
 
   // the rows' positions and the keys [0, n_keys) that any of them sees
-  const int pos0 = c.pos[b];
   const int64_t cap = (int64_t)c.max_blocks * c.page_tokens;
   const int64_t my_row = r0 + g;
-  const int my_new = my_row < rows ? (int)(my_row / a.group) : 0;
+  const int my_new = my_row < rows ? (int)((uint32_t)my_row / (uint32_t)a.group) : 0;
   const int64_t my_pos = (int64_t)pos0 + my_new;
   const bool placed = my_row < rows && pos0 >= 0 && my_pos < c.rope_positions;
   const int last = placed ? (int)(my_pos < cap ? my_pos : cap - 1) : -1;  // the row's last key
   const int64_t lo_pos = pos0 + r0 / a.group, hi_pos = pos0 + (min(r0 + kRows, rows) - 1) / a.group;
   const int n_keys = pos0 < 0 ? 0 : (int)min(hi_pos + 1, cap);
   const int all_see = (int)min(lo_pos + 1, cap);  // keys below it are seen by every row that has a position
+  const int n_steps = (n_keys + kKeys - 1) / kKeys;
+  const int codes = c.page_tokens * G::kRowBytes;
+
+  uint8_t* ring = smem + warp * G::kWarpBytes;
+  float4* scales = reinterpret_cast<float4*>(ring + G::kStages * G::kStageBytes);
+  // Copies the step's keys to `stage`, as far as they have a place, moves on to
+  // the warp's next step, and says which runs came (4 bits).
+  auto issue = [&](uint8_t* stage) -> uint32_t {
+    const bool here = block >= 0 && block < c.n_blocks && key < n_keys;
+    const uint32_t came = __ballot_sync(0xFFFFFFFFu, here) & 15u;
+    const unsigned long long base = here ? reinterpret_cast<unsigned long long>(kv4_page(c, block, head)) : 0;
+    const int j = lane & 15, of_v = lane >> 4;  // 16 lanes copy K's (s, z), 16 V's: four keys each
+    uint8_t* sz = stage + 2 * kKeys * G::kRowBytes + lane * 16;
+    uint32_t held;
+    if (whole) {
+      const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, base, 0));
+      const int at = __shfl_sync(0xFFFFFFFFu, row, 0);
+      held = came & 1 ? 15u : 0;
+      if (page) {
+        const uint8_t* src = page + at * G::kRowBytes + lane * 16;
+        uint8_t* dst = stage + lane * 16;
+#pragma unroll
+        for (int o = 0; o < kKeys * G::kRowBytes; o += 512) {
+          cp16(dst + o, src + o);
+          cp16(dst + kKeys * G::kRowBytes + o, src + codes + o);
+        }
+        cp16(sz, page + 2 * codes + (of_v * c.page_tokens + at + 4 * j) * 4);
+      }
+    } else {
+      held = came;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, base, i));
+        const int at = __shfl_sync(0xFFFFFFFFu, row, i);
+        if (!page) continue;
+        const uint8_t* src = page + at * G::kRowBytes + lane * 16;
+        uint8_t* dst = stage + i * 16 * G::kRowBytes + lane * 16;
+#pragma unroll
+        for (int o = 0; o < 16 * G::kRowBytes; o += 512) {
+          cp16(dst + o, src + o);
+          cp16(dst + kKeys * G::kRowBytes + o, src + codes + o);
+        }
+      }
+      const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, base, j >> 2));
+      const int at = __shfl_sync(0xFFFFFFFFu, row, j >> 2);
+      if (page) cp16(sz, page + 2 * codes + (of_v * c.page_tokens + at + 4 * (j & 3)) * 4);
+    }
+    cp_commit();
+    key += ahead;
+    slot += skip_slots;
+    row += skip_rows;
+    if (row >= c.page_tokens) {
+      row -= c.page_tokens;
+      ++slot;
+    }
+    block = ask();
+    return held;
+  };
+  uint32_t held = 0;  // 4 bits a stage: runs that came
+#pragma unroll
+  for (int s = 0; s < G::kStages - 1; ++s) held |= issue(ring + s * G::kStageBytes) << (4 * s);
 
   // Q: lane (g, t) holds dims 4 WPL t .. + 4 WPL of both halves of row g,
   // scaled by a power of two that brings the row's largest value to 2^13..2^14
@@ -159,8 +245,8 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
 #pragma unroll
     for (int i = 0; i < 4 * WPL; ++i) lo[i] = hi[i] = 0.f;
     if (placed) {
-      const T* p = q + (int64_t)(q0 + my_new) * a.q_tok + (head * a.group + (int)(my_row % a.group)) * a.q_head +
-                   4 * WPL * t;
+      const T* p = q + (int64_t)(q0 + my_new) * a.q_tok +
+                   (head * a.group + (int)((uint32_t)my_row % (uint32_t)a.group)) * a.q_head + 4 * WPL * t;
 #pragma unroll
       for (int i = 0; i < WPL; ++i) {
         load4(p + 4 * i, lo + 4 * i);
@@ -194,7 +280,7 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
     }
     const int up = top > 0.f && top < INFINITY ? min(13 - ilogbf(top), 120) : 0;
     const float mul = scalbnf(1.f, up);
-    logit_mul = scalbnf(a.scale_log2, (kFull ? 0 : 24) - up);
+    logit_mul = scalbnf(a.scale_log2, (P::kCentreK ? 0 : 24) - up);
     logit_z = a.scale_log2 * sum;
 #pragma unroll
     for (int k = 0; k < 2 * WPL; ++k) {
@@ -206,204 +292,138 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
         const uint32_t h = pack_f16(x, y);
         const float2 back = unpack_f16(h);
         qa[k][2 * odd] = h;
-        qa[k][2 * odd + 1] = pack_f16(x - back.x, y - back.y);
+        qa[k][2 * odd + 1] = P::kQLow ? pack_f16(x - back.x, y - back.y) : 0u;
       }
     }
   }
 
-  uint8_t* ring = smem + warp * (G::kStages * G::kStageBytes);
-  const int n_steps = (n_keys + kKeys - 1) / kKeys, stride = a.split * G::kWarps;
-  const int32_t* table = c.table + (int64_t)b * c.max_blocks;
-  const int codes = c.page_tokens * G::kRowBytes;
-
-  // A step's keys come in four runs of 16, each inside one page.  Lane i < 4
-  // looks run i up (a step ahead of the copies): its rows' place, or NULL.
-  struct Run {
-    const uint8_t* page;
-    int row;
-  };
-  auto look_up = [&](int step) {
-    Run r{nullptr, 0};
-    const int64_t key = (int64_t)step * kKeys + 16 * lane;
-    if (lane < 4 && step < n_steps && key < n_keys) {
-      const int slot = (int)key / c.page_tokens;
-      const int block = table[slot];
-      r.row = (int)key - slot * c.page_tokens;
-      if (block >= 0 && block < c.n_blocks) r.page = kv4_page(c, block, head);
-    }
-    return r;
-  };
-  auto issue = [&](const Run& mine, uint8_t* stage) {
-    const unsigned long long base = reinterpret_cast<unsigned long long>(mine.page);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, base, i));
-      const int row = __shfl_sync(0xFFFFFFFFu, mine.row, i);
-      if (!page) continue;
-      const uint8_t* src = page + row * G::kRowBytes + lane * 16;
-      uint8_t* dst = stage + i * 16 * G::kRowBytes + lane * 16;
-#pragma unroll
-      for (int o = 0; o < 16 * G::kRowBytes; o += 512) {
-        cp16(dst + o, src + o);
-        cp16(dst + kKeys * G::kRowBytes + o, src + codes + o);
-      }
-    }
-    // 16 lanes copy K's (s, z), 16 V's: four keys each
-    const int j = lane & 15, of_v = lane >> 4;
-    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, base, j >> 2));
-    const int row = __shfl_sync(0xFFFFFFFFu, mine.row, j >> 2);
-    if (page)
-      cp16(stage + 2 * kKeys * G::kRowBytes + lane * 16,
-           page + 2 * codes + (of_v * c.page_tokens + row + 4 * (j & 3)) * 4);
-  };
-
-  float m = -INFINITY, l = 0.f, pz = 0.f;  // of row g (pz: of p y); l and pz of this lane's keys only
-  float o[2 * WPL][4];                     // rows 2t, 2t + 1: dims 4g + .. of both halves (word g, word g + 8)
+  // Running sums of the online softmax, all of them 2^-off times the true ones:
+  // off = m - (14 - exponent of the largest V scale so far), so that P s, which
+  // the second product takes in fp16, stays below 2^15 whatever the scales (one
+  // below 2^-86 counts as 2^-86).
+  float m = -INFINITY, off = 0.f, l = 0.f, py = 0.f;  // of row g; l and py (sum of p y) of this lane's keys only
+  float o[2 * WPL][4];                                // rows 2t, 2t + 1: dims 4g + .. of both halves
 #pragma unroll
   for (int i = 0; i < 2 * WPL; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  // exponent field of the largest V scale so far: P s is kept times 2^14 over
-  // that scale's power of two, so that it stays inside fp16 whatever the scales
-  // (a scale below 2^-113 counts as 2^-113)
-  uint32_t v_exp = 14;
-
-  int step = rank * G::kWarps + warp;
-  uint32_t held = 0;  // 4 bits a stage: runs that have a place
-  Run next = look_up(step);
-#pragma unroll
-  for (int s = 0; s < G::kStages - 1; ++s) {
-    held |= (__ballot_sync(0xFFFFFFFFu, next.page != nullptr) & 15u) << (4 * s);
-    issue(next, ring + s * G::kStageBytes);
-    cp_commit();
-    next = look_up(step + (s + 1) * stride);
-  }
+  uint32_t v_exp = 41;
   int cur = 0;
-  for (; step < n_steps; step += stride) {
+#pragma unroll 1
+  for (int step = first; step < n_steps; step += stride) {
     cp_wait<G::kStages - 2>();
     __syncwarp();
     {  // every lane is done with the previous step's stage: refill it
       const int to = cur == 0 ? G::kStages - 1 : cur - 1;
-      held = (held & ~(15u << (4 * to))) | ((__ballot_sync(0xFFFFFFFFu, next.page != nullptr) & 15u) << (4 * to));
-      issue(next, ring + to * G::kStageBytes);
-      cp_commit();
-      next = look_up(step + G::kStages * stride);
+      held = (held & ~(15u << (4 * to))) | issue(ring + to * G::kStageBytes) << (4 * to);
     }
     const uint8_t* stage = ring + cur * G::kStageBytes;
     const uint32_t have = (held >> (4 * cur)) & 15u;
     cur = cur + 1 == G::kStages ? 0 : cur + 1;
     const int key0 = step * kKeys;
 
-    // S
-    float s[8][4];
+    // the step's scales as floats, two keys a lane: K's s and offset, V's s and y;
+    // zeros for keys without a place (whatever the stage held)
+    uint32_t s_top = 0;
+    {
+      const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * kKeys * G::kRowBytes);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = lane + 32 * i;
+        const bool there = ((have >> (j >> 4)) & 1u) && key0 + j < n_keys;
+        const uint32_t kw = there ? ksz[j] : 0u, vw = there ? ksz[kKeys + j] : 0u;
+        const float ks = __uint_as_float(kw << 16), vs = __uint_as_float(vw << 16);
+        scales[j] = make_float4(ks, fmaf(P::kCentreK ? 8.f : 0.f, ks, __uint_as_float(kw & 0xFFFF0000u)), vs,
+                                fmaf(P::kCentreV ? 8.f : 0.f, vs, __uint_as_float(vw & 0xFFFF0000u)));
+        s_top = max(s_top, vw << 16);
+      }
+      s_top = __reduce_max_sync(0xFFFFFFFFu, s_top);  // and the scales are written
+    }
+    __syncwarp();
+
+    // S, and the logits in units of log2
+    float x[16];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      const int key = 8 * n + (g & 1 ? 7 - (g >> 1) : g >> 1);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      const int at = 8 * n + (g & 1 ? 7 - (g >> 1) : g >> 1);
       uint32_t w[WPL];
       if (WPL == 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(stage + key * G::kRowBytes + t * 8);
+        const uint2 v = *reinterpret_cast<const uint2*>(stage + at * G::kRowBytes + t * 8);
         w[0] = v.x, w[1] = v.y;
       } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + key * G::kRowBytes + t * 16);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + at * G::kRowBytes + t * 16);
         w[0] = v.x, w[1] = v.y, w[WPL - 2] = v.z, w[WPL - 1] = v.w;
       }
 #pragma unroll
       for (int i = 0; i < WPL; ++i) {
         const uint32_t h = w[i] >> 8;
-        const uint32_t k0 = kFull ? centred_even(w[i]) : w[i] & kEven, k1 = kFull ? centred_odd(w[i]) : w[i] & kOdd;
-        const uint32_t k2 = kFull ? centred_even(h) : h & kEven, k3 = kFull ? centred_odd(h) : h & kOdd;
-        mma16816(s[n], qa[2 * i][0], qa[2 * i][1], qa[2 * i][2], qa[2 * i][3], k0, k1);
-        mma16816(s[n], qa[2 * i + 1][0], qa[2 * i + 1][1], qa[2 * i + 1][2], qa[2 * i + 1][3], k2, k3);
+        const uint32_t k0 = P::kCentreK ? centred_even(w[i]) : w[i] & kEven;
+        const uint32_t k1 = P::kCentreK ? centred_odd(w[i]) : w[i] & kOdd;
+        const uint32_t k2 = P::kCentreK ? centred_even(h) : h & kEven, k3 = P::kCentreK ? centred_odd(h) : h & kOdd;
+        mma16816(s, qa[2 * i][0], qa[2 * i][1], qa[2 * i][2], qa[2 * i][3], k0, k1);
+        mma16816(s, qa[2 * i + 1][0], qa[2 * i + 1][1], qa[2 * i + 1][2], qa[2 * i + 1][3], k2, k3);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 ks = *reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]);
+        const float dot = P::kQLow ? s[e] + s[2 + e] : s[e];
+        x[2 * n + e] = fmaf(ks.x, dot * logit_mul, ks.y * logit_z);
       }
     }
-    const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * kKeys * G::kRowBytes);
-    const uint32_t* vsz = ksz + kKeys;
-    float x[16];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t sz = ksz[8 * n + (e ? 7 - t : t)];
-        const float ks = __uint_as_float(sz << 16);
-        const float kz = fmaf(kFull ? 8.f : 0.f, ks, __uint_as_float(sz & 0xFFFF0000u));
-        x[2 * n + e] = fmaf(ks, (s[n][e] + s[n][2 + e]) * logit_mul, kz * logit_z);
-      }
-    float vs[16], vz[16];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t sz = vsz[8 * n + (e ? 7 - t : t)];
-        vs[2 * n + e] = __uint_as_float(sz << 16);
-        vz[2 * n + e] = fmaf(8.f, vs[2 * n + e], __uint_as_float(sz & 0xFFFF0000u));
-      }
-    if (have != 15u || key0 + kKeys > all_see) {
-      // keys without a place, or behind a row's last one: their score is left
-      // out, and whatever their rows hold (or the stage held) reads as zero
+    const bool part = have != 15u || key0 + kKeys > all_see;
+    if (part) {  // scores without a place, or behind the row's last key
 #pragma unroll
       for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = key0 + 8 * n + (e ? 7 - t : t);
-          const bool there = (have >> (n >> 1)) & 1u;
-          if (!there || key >= n_keys) vs[2 * n + e] = vz[2 * n + e] = 0.f;
-          if (!there || key > last) {
-            x[2 * n + e] = -INFINITY;
-            vz[2 * n + e] = 0.f;
-          }
-        }
+        for (int e = 0; e < 2; ++e)
+          if (!((have >> (n >> 1)) & 1u) || key0 + 8 * n + (e ? 7 - t : t) > last) x[2 * n + e] = -INFINITY;
     }
 
-    // softmax of row g over the step's keys, and the running normalisers
+    // softmax of row g over the step's keys
     float top = x[0];
-    uint32_t s_top = __float_as_uint(vs[0]);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) {
-      top = fmaxf(top, x[i]);
-      s_top = max(s_top, __float_as_uint(vs[i]));
-    }
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const uint32_t e_new = max(v_exp, min(__reduce_max_sync(0xFFFFFFFFu, s_top) >> 23, 254u));
+    const uint32_t e_new = max(v_exp, min(s_top >> 23, 254u));
     const float m_new = fmaxf(m, top);
-    const bool moved = m_new != m || e_new != v_exp;
-    const float m_use = m_new == -INFINITY ? 0.f : m_new;
-    if (__any_sync(0xFFFFFFFFu, moved)) {
-      const float fade = ex2(m - m_use);
-      l *= fade;
-      pz *= fade;
-      const float drop = scalbnf(1.f, max((int)v_exp - (int)e_new, -126));
-      const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t) * drop;
-      const float f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4) * drop;
+    if (__any_sync(0xFFFFFFFFu, m_new != m || e_new != v_exp)) {
+      const float off_new = (m_new == -INFINITY ? 0.f : m_new) - (float)(141 - (int)e_new);  // 14 + 127
+      const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
+      l *= fade;  // a NaN stays
+      py *= fade;
+      const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4);
 #pragma unroll
       for (int i = 0; i < 2 * WPL; ++i) {
         o[i][0] *= f0, o[i][2] *= f0;
         o[i][1] *= f1, o[i][3] *= f1;
       }
       m = m_new;
+      off = off_new;
       v_exp = e_new;
     }
-    const float unit = __uint_as_float((268u - v_exp) << 23);  // 2^(14 - exponent)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p = ex2(x[i] - m_use);
-      l += p;
-      pz = fmaf(p, vz[i], pz);
-      x[i] = p * (vs[i] * unit);
-    }
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 vs = *(reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]) + 1);
+        const float p = ex2(x[2 * n + e] - off);
+        l += p;
+        // a key that the row does not see must not count, even with an offset of NaN
+        py = part && x[2 * n + e] == -INFINITY ? py : fmaf(p, vs.y, py);
+        x[2 * n + e] = p * vs.x;
+      }
 
-    // O^T += V^T P^T, 16 keys at a time.  The tensor pipe cuts off what its sums
-    // cannot hold: where 22 bits are kept, a step's sum is its own and joins the
-    // running one in a rounded addition.
-    float step_o[2 * WPL][4];
-    if (kFull) {
+    // O^T += V^T P^T, 16 keys at a time
+    float own[2 * WPL][4];
+    if (P::kOwnSums) {
 #pragma unroll
-      for (int i = 0; i < 2 * WPL; ++i) step_o[i][0] = step_o[i][1] = step_o[i][2] = step_o[i][3] = 0.f;
+      for (int i = 0; i < 2 * WPL; ++i) own[i][0] = own[i][1] = own[i][2] = own[i][3] = 0.f;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t b0 = pack_f16(x[4 * k], x[4 * k + 1]), b1 = pack_f16(x[4 * k + 2], x[4 * k + 3]);
       uint32_t d0 = 0, d1 = 0;
-      if (kFull) {
+      if (P::kPLow) {
         const float2 r0 = unpack_f16(b0), r1 = unpack_f16(b1);
         d0 = pack_f16(x[4 * k] - r0.x, x[4 * k + 1] - r0.y);
         d1 = pack_f16(x[4 * k + 2] - r1.x, x[4 * k + 3] - r1.y);
@@ -419,9 +439,9 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
       } else {
         // rows of 16 words: half of the lanes take their second word first, so
         // that the four rows of a load do not meet in a bank
-        const int first = g + 8 * (t >> 1), second = first ^ 8;
-        uint32_t u[4] = {v0[first], v1[first], v2[first], v3[first]};
-        uint32_t y[4] = {v0[second], v1[second], v2[second], v3[second]};
+        const int f = g + 8 * (t >> 1), h = f ^ 8;
+        uint32_t u[4] = {v0[f], v1[f], v2[f], v3[f]};
+        uint32_t y[4] = {v0[h], v1[h], v2[h], v3[h]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           w[0][i] = t < 2 ? u[i] : y[i];
@@ -436,28 +456,31 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
           uint32_t a23 = __byte_perm(w[i][2], w[i][3], half ? 0x7632 : 0x5410);
 #pragma unroll
           for (int pair = 0; pair < 2; ++pair) {
-            float(&d)[4] = kFull ? step_o[4 * i + 2 * half + pair] : o[4 * i + 2 * half + pair];
-            const uint32_t e0 = centred_even(a01), e1 = centred_odd(a01), e2 = centred_even(a23), e3 = centred_odd(a23);
+            float(&d)[4] = P::kOwnSums ? own[4 * i + 2 * half + pair] : o[4 * i + 2 * half + pair];
+            const uint32_t e0 = P::kCentreV ? centred_even(a01) : a01 & kEven;
+            const uint32_t e1 = P::kCentreV ? centred_odd(a01) : a01 & kOdd;
+            const uint32_t e2 = P::kCentreV ? centred_even(a23) : a23 & kEven;
+            const uint32_t e3 = P::kCentreV ? centred_odd(a23) : a23 & kOdd;
             mma16816(d, e0, e1, e2, e3, b0, b1);
-            if (kFull) mma16816(d, e0, e1, e2, e3, d0, d1);
+            if (P::kPLow) mma16816(d, e0, e1, e2, e3, d0, d1);
             a01 >>= 8;
             a23 >>= 8;
           }
         }
       }
     }
-    if (kFull) {
+    if (P::kOwnSums) {
 #pragma unroll
       for (int i = 0; i < 2 * WPL; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] += step_o[i][e];
+        for (int e = 0; e < 4; ++e) o[i][e] += own[i][e];
     }
   }
   cp_wait<0>();
 #pragma unroll
   for (int d = 1; d < 4; d <<= 1) {
     l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-    pz += __shfl_xor_sync(0xFFFFFFFFu, pz, d);
+    py += __shfl_xor_sync(0xFFFFFFFFu, py, d);
   }
 
   // join the warps, then the cluster's CTAs
@@ -465,7 +488,7 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
   float* part = reinterpret_cast<float*>(smem);
   {
     float* mine = part + warp * G::kWarpPart;
-    const float even = scalbnf(1.f, (int)v_exp - 127 - 14);  // one over the power of two that P s carries
+    const float even = P::kCentreV ? 1.f : 16777216.f;  // raw codes stand at 2^-24
 #pragma unroll
     for (int i = 0; i < 2 * WPL; ++i) {
       // o[i]: word g + 8 (i / 4) of the row, its half (i / 2) % 2, nibble pair i % 2
@@ -477,93 +500,126 @@ __global__ void __launch_bounds__(Geo<HD>::kWarps * 32)
       r[HD + 1] = o[i][3] * (even * 0.0625f);
     }
     if (t == 0) {
-      mine[kRows * HD + g] = m;
+      mine[kRows * HD + g] = m == -INFINITY ? -INFINITY : off;
       mine[kRows * HD + kRows + g] = l;
-      mine[kRows * HD + 2 * kRows + g] = pz;
+      mine[kRows * HD + 2 * kRows + g] = py;
     }
   }
   __syncthreads();
-  float* cta = part + G::kWarps * G::kWarpPart;  // O [row][HD], then m, then l
-  for (int e = threadIdx.x; e < kRows * HD; e += G::kWarps * 32) {
-    const int row = e / HD;
+  // a row that saw no key, or has no rotation, answers zeros
+  auto store = [&](int e, float sum, float all) {
+    const int rw = e / HD;
+    if (r0 + rw >= rows) return;
+    const uint32_t fresh = (uint32_t)(r0 + rw) / (uint32_t)a.group, h = (uint32_t)(r0 + rw) % (uint32_t)a.group;
+    const float y = all == 0.f || (int64_t)pos0 + fresh >= c.rope_positions ? 0.f : sum / all;
+    T* dst = out + (int64_t)(q0 + (int)fresh) * a.o_tok + (head * a.group + (int)h) * a.o_head + e % HD;
+    if constexpr (P::kFp32)
+      *dst = y;
+    else if constexpr (P::kBf16)
+      *dst = __float2bfloat16_rn(y);
+    else
+      *dst = __float2half_rn(y);
+  };
+  float* cta = part + WARPS * G::kWarpPart;  // O [row][HD], then the offsets, then l
+#pragma unroll 1
+  for (int e = threadIdx.x; e < kRows * HD; e += WARPS * 32) {
+    const int rw = e / HD;
     float top = -INFINITY, sum = 0.f, all = 0.f;
 #pragma unroll
-    for (int w = 0; w < G::kWarps; ++w) top = fmaxf(top, part[w * G::kWarpPart + kRows * HD + row]);
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, part[w * G::kWarpPart + kRows * HD + rw]);
 #pragma unroll
-    for (int w = 0; w < G::kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float* p = part + w * G::kWarpPart;
-      const float mw = p[kRows * HD + row];
+      const float mw = p[kRows * HD + rw];
       const float f = mw == top ? 1.f : ex2(mw - top);  // no key yet anywhere: sums of zeros
-      sum = fmaf(f, p[e] + p[kRows * HD + 2 * kRows + row], sum);
-      all = fmaf(f, p[kRows * HD + kRows + row], all);
+      sum = fmaf(f, p[e] + p[kRows * HD + 2 * kRows + rw], sum);
+      all = fmaf(f, p[kRows * HD + kRows + rw], all);
+    }
+    if (a.split == 1) {
+      store(e, sum, all);
+      continue;
     }
     cta[e] = sum;
     if (e % HD == 0) {
-      cta[kRows * HD + row] = top;
-      cta[kRows * HD + kRows + row] = all;
+      cta[kRows * HD + rw] = top;
+      cta[kRows * HD + kRows + rw] = all;
     }
   }
-  cg::cluster_group cluster = cg::this_cluster();
+  if (a.split == 1) return;
   cluster_barrier();
-  for (int e = rank * G::kWarps * 32 + threadIdx.x; e < kRows * HD; e += a.split * G::kWarps * 32) {
-    const int row = e / HD;
-    float top = -INFINITY, sum = 0.f, all = 0.f;
-    for (int r = 0; r < a.split; ++r) top = fmaxf(top, cluster.map_shared_rank(cta, r)[kRows * HD + row]);
-    for (int r = 0; r < a.split; ++r) {
-      const float* p = cluster.map_shared_rank(cta, r);
-      const float mr = p[kRows * HD + row];
-      const float f = mr == top ? 1.f : ex2(mr - top);
-      sum = fmaf(f, p[e], sum);
-      all = fmaf(f, p[kRows * HD + kRows + row], all);
+#pragma unroll 1
+  for (int e = rank * WARPS * 32 + threadIdx.x; e < kRows * HD; e += a.split * WARPS * 32) {
+    const int rw = e / HD;
+    float part_o[kMaxSplit], part_m[kMaxSplit], part_l[kMaxSplit], top = -INFINITY, sum = 0.f, all = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) {  // all on their way at once
+      const bool on = r < a.split;
+      part_m[r] = on ? __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + rw, r))) : -INFINITY;
+      part_l[r] = on ? __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + kRows + rw, r))) : 0.f;
+      part_o[r] = on ? __uint_as_float(cluster_load32(cluster_address(cta + e, r))) : 0.f;
     }
-    if (r0 + row < rows) {
-      const int64_t fresh = (r0 + row) / a.group;
-      // a row that saw no key, or has no rotation, answers zeros
-      const float y = all == 0.f || pos0 + fresh >= c.rope_positions ? 0.f : sum / all;
-      T* dst = out + (q0 + fresh) * a.o_tok + (head * a.group + (int)((r0 + row) % a.group)) * a.o_head + e % HD;
-      if constexpr (sizeof(T) == 4)
-        *dst = y;
-      else if constexpr (std::is_same<T, __half>::value)
-        *dst = __float2half_rn(y);
-      else
-        *dst = __float2bfloat16_rn(y);
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) top = fmaxf(top, part_m[r]);
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) {
+      const float f = part_m[r] == top ? 1.f : ex2(part_m[r] - top);
+      sum = fmaf(f, part_o[r], sum);
+      all = fmaf(f, part_l[r], all);
     }
+    store(e, sum, all);
   }
   cluster_barrier();  // no CTA leaves while another reads its part
 }
 
 // Per device, once: the kernel's shared-memory limit and cluster size.
-template <typename T, int HD>
+template <typename T, int HD, int WARPS>
 cudaError_t prepare() {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
-  const void* fn = reinterpret_cast<const void*>(&kv4_attention_kernel<T, HD>);
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<HD>::kSmem);
+  const void* fn = reinterpret_cast<const void*>(&kv4_attention_kernel<T, HD, WARPS>);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<HD, WARPS>::kSmem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
   return e;
 }
 
-template <typename T, int HD>
-cudaError_t launch(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, AttnArgs a, int64_t items,
+template <typename T, int HD, int WARPS>
+cudaError_t launch(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, const AttnArgs& a, int64_t items,
                    cudaStream_t s) {
-  cudaError_t e = prepare<T, HD>();
+  cudaError_t e = prepare<T, HD, WARPS>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * a.split));
-  cfg.blockDim = dim3(Geo<HD>::kWarps * 32);
-  cfg.dynamicSmemBytes = Geo<HD>::kSmem;
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = Geo<HD, WARPS>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = a.split;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_attention_kernel<T, HD>, d, static_cast<const T*>(q.p),
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kv4_attention_kernel<T, HD, WARPS>, d, static_cast<const T*>(q.p),
                             static_cast<T*>(const_cast<void*>(o.p)), a);
+}
+
+// CTAs that share a row block's keys: enough to fill the GPU (148 SMs), no more
+// than leave a warp two steps of 64 keys.
+template <typename T, int HD>
+cudaError_t choose(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, AttnArgs a, int64_t items,
+                   cudaStream_t s) {
+  const int64_t steps = ((int64_t)d.max_blocks * d.page_tokens + kKeys - 1) / kKeys;
+  auto split = [&](int64_t ctas, int warps) {
+    int n = 1;
+    while (n < kMaxSplit && items * n < ctas && steps >= (int64_t)n * 2 * warps * 2) n *= 2;
+    return n;
+  };
+  // 16 CTAs of 4 warps for each: would they leave more than half of the GPU idle?
+  const bool wide = items * kMaxSplit * 2 < 148 * Geo<HD, 4>::kPerSm && steps >= kMaxSplit * 12 * 2;
+  a.split = wide ? split(148, 12) : split(148 * Geo<HD, 4>::kPerSm, 4);
+  return wide ? launch<T, HD, 12>(d, q, o, a, items, s) : launch<T, HD, 4>(d, q, o, a, items, s);
 }
 
 }  // namespace
@@ -580,21 +636,17 @@ int kv4_attention_launch(const Kv4Dev& d, int head_dim, int max_new, const Kv4Te
   a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)head_dim) : scale) * 1.4426950408889634f;
   const int64_t row_blocks = ((int64_t)a.max_new * a.group + kRows - 1) / kRows;
   const int64_t items = row_blocks * d.n_kv * d.batch;
-  if (items > INT_MAX / 16) return op_fail(WPK_ERR_SHAPE, "too many query rows for one call");
+  if (row_blocks * kRows > INT_MAX || items > INT_MAX / kMaxSplit)
+    return op_fail(WPK_ERR_SHAPE, "too many query rows for one call");
   a.row_blocks = (int)row_blocks;
-  // CTAs that share a row block's keys: enough to fill the SMs (two CTAs each
-  // at head_dim 64), and no more than have a step of 64 keys per warp
-  const int64_t longest = ((int64_t)d.max_blocks * d.page_tokens + kKeys - 1) / kKeys;
-  a.split = 1;
-  while (a.split < 16 && items * a.split < 148 && longest > (int64_t)a.split * 8) a.split *= 2;
   cudaError_t e;
   const bool wide = head_dim == 128;
   if (dtype == WPK_F32)
-    e = wide ? launch<float, 128>(d, q, out, a, items, s) : launch<float, 64>(d, q, out, a, items, s);
+    e = wide ? choose<float, 128>(d, q, out, a, items, s) : choose<float, 64>(d, q, out, a, items, s);
   else if (dtype == WPK_BF16)
-    e = wide ? launch<__nv_bfloat16, 128>(d, q, out, a, items, s) : launch<__nv_bfloat16, 64>(d, q, out, a, items, s);
+    e = wide ? choose<__nv_bfloat16, 128>(d, q, out, a, items, s) : choose<__nv_bfloat16, 64>(d, q, out, a, items, s);
   else
-    e = wide ? launch<__half, 128>(d, q, out, a, items, s) : launch<__half, 64>(d, q, out, a, items, s);
+    e = wide ? choose<__half, 128>(d, q, out, a, items, s) : choose<__half, 64>(d, q, out, a, items, s);
   if (e != cudaSuccess) {
     char msg[160];
     snprintf(msg, sizeof msg, "wpk_kv4_attention: %s", cudaGetErrorString(e));
