@@ -236,10 +236,11 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
 #pragma unroll
   for (int s = 0; s < G::kStages - 1; ++s) held |= issue(ring + s * G::kStageBytes) << (4 * s);
 
-  // Q: lane (g, t) holds dims 4 WPL t .. + 4 WPL of both halves of row g,
-  // scaled by a power of two that brings the row's largest value to 2^13..2^14
+  // Q: lane (g, t) holds dims 4 WPL t .. + 4 WPL of both halves of row g, times
+  // scale log2(e) and a power of two that brings the rows' largest value to
+  // 2^13..2^14; K's scales take it back
   uint32_t qa[2 * WPL][4];
-  float logit_mul, logit_z;
+  float k_mul, logit_z;
   {
     float lo[4 * WPL], hi[4 * WPL];
 #pragma unroll
@@ -270,18 +271,19 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     float top = 0.f, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * WPL; ++i) {
+      lo[i] *= a.scale_log2;
+      hi[i] *= a.scale_log2;
       top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
       sum += lo[i] + hi[i];
     }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    }
-    const int up = top > 0.f && top < INFINITY ? min(13 - ilogbf(top), 120) : 0;
-    const float mul = scalbnf(1.f, up);
-    logit_mul = scalbnf(a.scale_log2, (P::kCentreK ? 0 : 24) - up);
-    logit_z = a.scale_log2 * sum;
+    for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    logit_z = sum;
+    // exponent fields: the power of two is 2^(140 - e), within fp32 (rows of no
+    // finite value, or below 2^-100, as they are)
+    const uint32_t e = max(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)) >> 23, 27u);
+    const float mul = __uint_as_float(e < 255u ? (267u - e) << 23 : 0x3F800000u);
+    k_mul = (P::kCentreK ? 1.f : 16777216.f) / mul;
 #pragma unroll
     for (int k = 0; k < 2 * WPL; ++k) {
 #pragma unroll
@@ -331,8 +333,9 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
         const bool there = ((have >> (j >> 4)) & 1u) && key0 + j < n_keys;
         const uint32_t kw = there ? ksz[j] : 0u, vw = there ? ksz[kKeys + j] : 0u;
         const float ks = __uint_as_float(kw << 16), vs = __uint_as_float(vw << 16);
-        scales[j] = make_float4(ks, fmaf(P::kCentreK ? 8.f : 0.f, ks, __uint_as_float(kw & 0xFFFF0000u)), vs,
-                                fmaf(P::kCentreV ? 8.f : 0.f, vs, __uint_as_float(vw & 0xFFFF0000u)));
+        const float kz = __uint_as_float(kw & 0xFFFF0000u), vz = __uint_as_float(vw & 0xFFFF0000u);
+        scales[j] = make_float4(ks * k_mul, P::kCentreK ? fmaf(8.f, ks, kz) : kz, vs,
+                                P::kCentreV ? fmaf(8.f, vs, vz) : vz);
         s_top = max(s_top, vw << 16);
       }
       s_top = __reduce_max_sync(0xFFFFFFFFu, s_top);  // and the scales are written
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       for (int e = 0; e < 2; ++e) {
         const float2 ks = *reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]);
         const float dot = P::kQLow ? s[e] + s[2 + e] : s[e];
-        x[2 * n + e] = fmaf(ks.x, dot * logit_mul, ks.y * logit_z);
+        x[2 * n + e] = fmaf(ks.x, dot, ks.y * logit_z);
       }
     }
     const bool part = have != 15u || key0 + kKeys > all_see;
@@ -401,17 +404,23 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       off = off_new;
       v_exp = e_new;
     }
+    auto weigh = [&](bool some) {
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+      for (int n = 0; n < 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 vs = *(reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]) + 1);
-        const float p = ex2(x[2 * n + e] - off);
-        l += p;
-        // a key that the row does not see must not count, even with an offset of NaN
-        py = part && x[2 * n + e] == -INFINITY ? py : fmaf(p, vs.y, py);
-        x[2 * n + e] = p * vs.x;
-      }
+        for (int e = 0; e < 2; ++e) {
+          const float2 vs = *(reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]) + 1);
+          const float p = ex2(x[2 * n + e] - off);
+          l += p;
+          // a key that the row does not see must not count, even with an offset of NaN
+          py = some && x[2 * n + e] == -INFINITY ? py : fmaf(p, vs.y, py);
+          x[2 * n + e] = p * vs.x;
+        }
+    };
+    if (part)
+      weigh(true);
+    else
+      weigh(false);
 
     // O^T += V^T P^T, 16 keys at a time
     float own[2 * WPL][4];
@@ -550,21 +559,18 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
 #pragma unroll 1
   for (int e = rank * WARPS * 32 + threadIdx.x; e < kRows * HD; e += a.split * WARPS * 32) {
     const int rw = e / HD;
-    float part_o[kMaxSplit], part_m[kMaxSplit], part_l[kMaxSplit], top = -INFINITY, sum = 0.f, all = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMaxSplit; ++r) {  // all on their way at once
-      const bool on = r < a.split;
-      part_m[r] = on ? __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + rw, r))) : -INFINITY;
-      part_l[r] = on ? __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + kRows + rw, r))) : 0.f;
-      part_o[r] = on ? __uint_as_float(cluster_load32(cluster_address(cta + e, r))) : 0.f;
-    }
-#pragma unroll
-    for (int r = 0; r < kMaxSplit; ++r) top = fmaxf(top, part_m[r]);
-#pragma unroll
-    for (int r = 0; r < kMaxSplit; ++r) {
-      const float f = part_m[r] == top ? 1.f : ex2(part_m[r] - top);
-      sum = fmaf(f, part_o[r], sum);
-      all = fmaf(f, part_l[r], all);
+    float top = -INFINITY, sum = 0.f, all = 0.f;
+#pragma unroll 4
+    for (int r = 0; r < a.split; ++r)
+      top = fmaxf(top, __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + rw, r))));
+#pragma unroll 4
+    for (int r = 0; r < a.split; ++r) {
+      const float mr = __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + rw, r)));
+      const float lr = __uint_as_float(cluster_load32(cluster_address(cta + kRows * HD + kRows + rw, r)));
+      const float po = __uint_as_float(cluster_load32(cluster_address(cta + e, r)));
+      const float f = mr == top ? 1.f : ex2(mr - top);
+      sum = fmaf(f, po, sum);
+      all = fmaf(f, lr, all);
     }
     store(e, sum, all);
   }
@@ -613,7 +619,7 @@ cudaError_t choose(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, Attn
   const int64_t steps = ((int64_t)d.max_blocks * d.page_tokens + kKeys - 1) / kKeys;
   auto split = [&](int64_t ctas, int warps) {
     int n = 1;
-    while (n < kMaxSplit && items * n < ctas && steps >= (int64_t)n * 2 * warps * 2) n *= 2;
+    while (n < kMaxSplit && items * n * 2 <= ctas && steps >= (int64_t)n * 2 * warps * 2) n *= 2;
     return n;
   };
   // 16 CTAs of 4 warps for each: would they leave more than half of the GPU idle?
