@@ -83,6 +83,42 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two floats in one instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -303,8 +339,9 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
   // off = m - (14 - exponent of the largest V scale so far), so that P s, which
   // the second product takes in fp16, stays below 2^15 whatever the scales (one
   // below 2^-86 counts as 2^-86).
-  float m = -INFINITY, off = 0.f, l = 0.f, py = 0.f;  // of row g; l and py (sum of p y) of this lane's keys only
-  float o[2 * WPL][4];                                // rows 2t, 2t + 1: dims 4g + .. of both halves
+  float m = -INFINITY, off = 0.f;  // of row g
+  F2 l2 = pair(0.f, 0.f), py2 = l2;  // l and the sum of p y, of this lane's keys only, in two halves
+  float o[2 * WPL][4];               // rows 2t, 2t + 1: dims 4g + .. of both halves
 #pragma unroll
   for (int i = 0; i < 2 * WPL; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   uint32_t v_exp = 41;
@@ -322,28 +359,31 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     cur = cur + 1 == G::kStages ? 0 : cur + 1;
     const int key0 = step * kKeys;
 
-    // the step's scales as floats, two keys a lane: K's s and offset, V's s and y;
-    // zeros for keys without a place (whatever the stage held)
-    uint32_t s_top = 0;
+    // the step's scales as floats: lane 4 n + t's keys are 8 n + t and 8 n + 7 - t,
+    // as S's columns have them; zeros for keys without a place (whatever the stage
+    // held)
+    uint32_t s_top;
     {
       const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * kKeys * G::kRowBytes);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = lane + 32 * i;
-        const bool there = ((have >> (j >> 4)) & 1u) && key0 + j < n_keys;
-        const uint32_t kw = there ? ksz[j] : 0u, vw = there ? ksz[kKeys + j] : 0u;
-        const float ks = __uint_as_float(kw << 16), vs = __uint_as_float(vw << 16);
-        const float kz = __uint_as_float(kw & 0xFFFF0000u), vz = __uint_as_float(vw & 0xFFFF0000u);
-        scales[j] = make_float4(ks * k_mul, P::kCentreK ? fmaf(8.f, ks, kz) : kz, vs,
-                                P::kCentreV ? fmaf(8.f, vs, vz) : vz);
-        s_top = max(s_top, vw << 16);
-      }
-      s_top = __reduce_max_sync(0xFFFFFFFFu, s_top);  // and the scales are written
+      const int ja = 8 * g + t, jb = 8 * g + 7 - t;
+      const bool there = (have >> (g >> 1)) & 1u;
+      const bool in_a = there && key0 + ja < n_keys, in_b = there && key0 + jb < n_keys;
+      const uint32_t ka = in_a ? ksz[ja] : 0u, kb = in_b ? ksz[jb] : 0u;
+      const uint32_t va = in_a ? ksz[kKeys + ja] : 0u, vb = in_b ? ksz[kKeys + jb] : 0u;
+      auto s_of = [](uint32_t w) { return __uint_as_float(w << 16); };
+      auto z_of = [](uint32_t w, bool centre) {
+        const float z = __uint_as_float(w & 0xFFFF0000u);
+        return centre ? fmaf(8.f, __uint_as_float(w << 16), z) : z;
+      };
+      scales[lane] = make_float4(s_of(ka) * k_mul, s_of(kb) * k_mul, z_of(ka, P::kCentreK), z_of(kb, P::kCentreK));
+      scales[32 + lane] = make_float4(s_of(va), s_of(vb), z_of(va, P::kCentreV), z_of(vb, P::kCentreV));
+      s_top = __reduce_max_sync(0xFFFFFFFFu, max(va << 16, vb << 16));
     }
     __syncwarp();
 
     // S, and the logits in units of log2
     float x[16];
+    const F2 z2 = pair(logit_z, logit_z);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -365,12 +405,12 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
         mma16816(s, qa[2 * i][0], qa[2 * i][1], qa[2 * i][2], qa[2 * i][3], k0, k1);
         mma16816(s, qa[2 * i + 1][0], qa[2 * i + 1][1], qa[2 * i + 1][2], qa[2 * i + 1][3], k2, k3);
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 ks = *reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]);
-        const float dot = P::kQLow ? s[e] + s[2 + e] : s[e];
-        x[2 * n + e] = fmaf(ks.x, dot, ks.y * logit_z);
-      }
+      const float4 ks = scales[4 * n + t];
+      F2 dot = pair(s[0], s[1]);
+      if (P::kQLow) dot = add2(dot, pair(s[2], s[3]));
+      const float2 xs = split(fma2(pair(ks.x, ks.y), dot, mul2(pair(ks.z, ks.w), z2)));
+      x[2 * n] = xs.x;
+      x[2 * n + 1] = xs.y;
     }
     const bool part = have != 15u || key0 + kKeys > all_see;
     if (part) {  // scores without a place, or behind the row's last key
@@ -382,9 +422,10 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     }
 
     // softmax of row g over the step's keys
-    float top = x[0];
+    float top = max3(x[0], x[1], x[2]);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+    for (int i = 3; i < 15; i += 2) top = max3(top, x[i], x[i + 1]);
+    top = fmaxf(top, x[15]);
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     const uint32_t e_new = max(v_exp, min(s_top >> 23, 254u));
@@ -392,8 +433,8 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     if (__any_sync(0xFFFFFFFFu, m_new != m || e_new != v_exp)) {
       const float off_new = (m_new == -INFINITY ? 0.f : m_new) - (float)(141 - (int)e_new);  // 14 + 127
       const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
-      l *= fade;  // a NaN stays
-      py *= fade;
+      l2 = mul2(l2, pair(fade, fade));  // a NaN stays
+      py2 = mul2(py2, pair(fade, fade));
       const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4);
 #pragma unroll
       for (int i = 0; i < 2 * WPL; ++i) {
@@ -404,23 +445,30 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       off = off_new;
       v_exp = e_new;
     }
-    auto weigh = [&](bool some) {
+    const F2 down = pair(-off, -off);
+    if (!part) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int n = 0; n < 8; ++n) {
+        const float4 vs = scales[32 + 4 * n + t];
+        const float2 d = split(add2(pair(x[2 * n], x[2 * n + 1]), down));
+        const F2 p = pair(ex2(d.x), ex2(d.y));
+        l2 = add2(l2, p);
+        py2 = fma2(p, pair(vs.z, vs.w), py2);
+        const float2 w = split(mul2(p, pair(vs.x, vs.y)));
+        x[2 * n] = w.x;
+        x[2 * n + 1] = w.y;
+      }
+    } else {  // a key that the row does not see must not count, even with an offset of NaN
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 vs = *(reinterpret_cast<const float2*>(&scales[8 * n + (e ? 7 - t : t)]) + 1);
-          const float p = ex2(x[2 * n + e] - off);
-          l += p;
-          // a key that the row does not see must not count, even with an offset of NaN
-          py = some && x[2 * n + e] == -INFINITY ? py : fmaf(p, vs.y, py);
-          x[2 * n + e] = p * vs.x;
-        }
-    };
-    if (part)
-      weigh(true);
-    else
-      weigh(false);
+      for (int n = 0; n < 8; ++n) {
+        const float4 vs = scales[32 + 4 * n + t];
+        const float pa = ex2(x[2 * n] - off), pb = ex2(x[2 * n + 1] - off);
+        l2 = add2(l2, pair(pa, pb));
+        py2 = fma2(pair(pa, pb), pair(x[2 * n] == -INFINITY ? 0.f : vs.z, x[2 * n + 1] == -INFINITY ? 0.f : vs.w), py2);
+        x[2 * n] = pa * vs.x;
+        x[2 * n + 1] = pb * vs.y;
+      }
+    }
 
     // O^T += V^T P^T, 16 keys at a time
     float own[2 * WPL][4];
@@ -482,10 +530,16 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
 #pragma unroll
       for (int i = 0; i < 2 * WPL; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] += own[i][e];
+        for (int e = 0; e < 4; e += 2) {
+          const float2 r = split(add2(pair(o[i][e], o[i][e + 1]), pair(own[i][e], own[i][e + 1])));
+          o[i][e] = r.x;
+          o[i][e + 1] = r.y;
+        }
     }
   }
   cp_wait<0>();
+  const float2 lp = split(l2), pp = split(py2);
+  float l = lp.x + lp.y, py = pp.x + pp.y;
 #pragma unroll
   for (int d = 1; d < 4; d <<= 1) {
     l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
