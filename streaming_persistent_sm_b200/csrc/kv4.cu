@@ -16,6 +16,7 @@ namespace wpk {
 namespace {
 
 constexpr int kThreadsKv4 = 128;
+constexpr int kHeads = 4;  // heads of a token that lanes take together
 
 // Sequence of token t: the last b with indptr[b] <= t, searched by the LANES
 // lanes of a row together (each round they probe LANES evenly spaced starts,
@@ -35,12 +36,12 @@ __device__ __forceinline__ int find_sequence(const Kv4Dev& c, int n_seq, int t, 
   return lo;
 }
 
-// Where row t of the call lives: its page (NULL: no place), its row in the
-// page and its position; false: the row belongs to no sequence.
+// Where token t of the call lives: its page id (-1: no place), its row in the
+// page and its position; false: the token belongs to no sequence.
 template <int LANES>
-__device__ __forceinline__ bool locate(const Kv4Dev& c, int t, int head, int j, uint32_t mask, uint8_t** page, int* row,
+__device__ __forceinline__ bool locate(const Kv4Dev& c, int t, int j, uint32_t mask, int* block, int* row,
                                        int* position) {
-  *page = nullptr;
+  *block = -1;
   *row = *position = 0;
   const int n_seq = kv4_sequences(c);
   int b, q0, n;
@@ -56,129 +57,233 @@ __device__ __forceinline__ bool locate(const Kv4Dev& c, int t, int head, int j, 
   const int64_t p = (int64_t)first + (t - q0);
   if (first < 0 || p >= (int64_t)c.max_blocks * c.page_tokens || p >= c.rope_positions) return true;
   const int slot = (int)p / c.page_tokens;
-  const int block = c.table[(int64_t)b * c.max_blocks + slot];
-  if (block < 0 || block >= c.n_blocks) return true;
-  *page = kv4_page(c, block, head);
+  const int id = c.table[(int64_t)b * c.max_blocks + slot];
+  if (id < 0 || id >= c.n_blocks) return true;
+  *block = id;
   *row = (int)p - slot * c.page_tokens;
   *position = (int)p;
   return true;
 }
 
 // The largest bf16 number <= x (as its bits), within the finite range.
-__device__ __forceinline__ uint32_t bf16_down(double x) {
-  uint32_t u = __float_as_uint(__double2float_rd(x));
+__device__ __forceinline__ uint32_t bf16_down(float x) {
+  uint32_t u = __float_as_uint(x);
   if (u & 0xFFFFu) u = (u & 0x80000000u) ? u + 0x10000u : u;  // away from zero below it
   u >>= 16;
   return u == 0xFF80u ? 0xFF7Fu : u;
 }
-
+__device__ __forceinline__ uint32_t bf16_near(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 // The bf16 number next to x >= 0, ties to even, rounded once: a float that is
 // not x itself gets an odd last bit, so that it never looks like a tie.
 __device__ __forceinline__ uint32_t bf16_near(double x) {
   float f = __double2float_rz(x);
   if ((double)f != x) f = __uint_as_float(__float_as_uint(f) | 1u);
-  return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+  return bf16_near(f);
 }
 
-__device__ __forceinline__ float lane_min(float a, float b) { return fminf(a, b); }
-__device__ __forceinline__ float lane_max(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ double lane_min(double a, double b) { return fmin(a, b); }
-__device__ __forceinline__ double lane_max(double a, double b) { return fmax(a, b); }
+// Codes of the lane's values from exact ones.
+__device__ __forceinline__ uint32_t exact_codes(const double (&x)[8], float z, float s) {
+  uint32_t w = 0;
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    double v = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v = i == e ? x[i] : v;  // registers have no index
+    const double c = s > 0.f ? rint((v - (double)z) / (double)s) : 0.0;
+    w |= (uint32_t)fmin(fmax(c, 0.0), 15.0) << (4 * e);
+  }
+  return w;
+}
 
-// Eight codes of this lane and the row's (s, z) word from the row's values, x
-// in a type R that holds them exactly (float as given, double when rotated).
-// The quotient (x - z) / s is computed in 32 bits, off by less than 3e-6; where
-// it comes within 1e-4 of a border between two codes it is computed again in 64.
-template <int LANES, typename R>
-__device__ __forceinline__ void quantise(const R (&x)[8], uint32_t mask, uint32_t* codes, uint32_t* sz) {
-  R lo = x[0], hi = x[0];
+// The lane's values in 64 bits: turned (each product is exact, the sum rounds
+// once), or as they are.
+template <bool kTurn>
+__device__ __forceinline__ void exact_values(const float (&a)[8], const float (&cs)[8], double (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double lo = a[e], hi = a[4 + e];
+    x[e] = kTurn ? lo * cs[2 * e] - hi * cs[2 * e + 1] : lo;
+    x[4 + e] = kTurn ? hi * cs[2 * e] + lo * cs[2 * e + 1] : hi;
+  }
+}
+
+// A row in 64 bits throughout.
+template <int LANES>
+__device__ __noinline__ uint2 quantise_exactly(const double (&x)[8], uint32_t mask) {
+  double lo = x[0], hi = x[0];
   bool fine = true;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    lo = lane_min(lo, x[e]);
-    hi = lane_max(hi, x[e]);
+    lo = fmin(lo, x[e]);
+    hi = fmax(hi, x[e]);
     fine = fine && isfinite(x[e]);
   }
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) {
-    lo = lane_min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    hi = lane_max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    lo = fmin(lo, __shfl_xor_sync(mask, lo, o));
+    hi = fmax(hi, __shfl_xor_sync(mask, hi, o));
   }
-  fine = (__ballot_sync(0xFFFFFFFFu, !fine) & mask) == 0;
-  if (!fine) {  // s = 0, z = NaN: the row reads as NaN
-    *codes = 0;
-    *sz = 0x7FC00000u;
-    return;
-  }
-  const uint32_t zb = bf16_down((double)lo);
+  if (__ballot_sync(mask, !fine) & mask) return make_uint2(0u, 0x7FC00000u);  // s = 0, z = NaN: reads as NaN
+  const uint32_t zb = bf16_down(__double2float_rd(lo));
   const float z = __uint_as_float(zb << 16);
-  const uint32_t sb = bf16_near(((double)hi - (double)z) / 15.0);
-  const float s = __uint_as_float(sb << 16);
-  const float inv = 1.0f / s;
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float t = (float)(x[e] - (R)z) * inv;
-    float c = rintf(t);
-    if (!(fabsf(fabsf(t - c) - 0.5f) > 1e-4f) || !(inv < 3e38f))  // near a border, or s too small for inv
-      c = s > 0.f ? (float)rint(((double)x[e] - (double)z) / (double)s) : 0.f;
-    w |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * e);
-  }
-  *codes = w;
-  *sz = sb | (zb << 16);
+  const uint32_t sb = bf16_near((hi - (double)z) / 15.0);
+  return make_uint2(exact_codes(x, z, __uint_as_float(sb << 16)), sb | zb << 16);
 }
 
-// Bound by bytes: a row comes in once and leaves as HD / 2 + 4 bytes.  The
-// rotation in 64 bits (two products and a sum a value, each product exact) makes
-// the codes those of exact arithmetic.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreadsKv4)
+// Eight codes of this lane and the row's (s, z) word, those of exact arithmetic.
+// The work is done in 32 bits with bounds: a turned value is off by at most 2^-23
+// of |a cos| + |b sin| (a product and a sum round), which 2 max |a| max |cos, sin|
+// bounds.  Where z or s could be
+// another bf16 number within the bounds (one row in some thousands), the row is
+// done again in 64 bits; where a quotient is as near to the border between two
+// codes, the lane's codes are (one turned value in 10^5).  Values that are not
+// turned lie on the border itself more often - 16-bit numbers, their distance
+// from z and s have few digits - and there the remainder x - z - c s decides,
+// which 32 bits hold exactly where they hold x - z.
+template <int LANES, bool kTurn>
+__device__ __forceinline__ void quantise(const float (&a)[8], const float (&cs)[8], uint32_t mask, uint32_t* codes,
+                                         uint32_t* sz) {
+  float x[8], bound = 0.f;
+  if (kTurn) {
+    float am = max3(fabsf(a[0]), fabsf(a[1]), fabsf(a[2])), cm = max3(fabsf(cs[0]), fabsf(cs[1]), fabsf(cs[2]));
+    am = max3(max3(am, fabsf(a[3]), fabsf(a[4])), fabsf(a[5]), fmaxf(fabsf(a[6]), fabsf(a[7])));
+    cm = max3(max3(cm, fabsf(cs[3]), fabsf(cs[4])), fabsf(cs[5]), fmaxf(fabsf(cs[6]), fabsf(cs[7])));
+    bound = 2.f * am * cm;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const F2 lo = pair(a[e], a[e + 1]), hi = pair(a[4 + e], a[5 + e]);
+      const F2 co = pair(cs[2 * e], cs[2 * e + 2]), si = pair(cs[2 * e + 1], cs[2 * e + 3]);
+      const F2 minus = pair(-cs[2 * e + 1], -cs[2 * e + 3]);
+      const float2 r = split(fma2(lo, co, mul2(hi, minus))), q = split(fma2(hi, co, mul2(lo, si)));
+      x[e] = r.x;
+      x[e + 1] = r.y;
+      x[4 + e] = q.x;
+      x[5 + e] = q.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = a[e];
+  }
+  float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), fminf(x[6], x[7]));
+  float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+  F2 none = pair(0.f, 0.f);  // a NaN where any value is one, or infinite
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) none = fma2(pair(x[e], x[e + 1]), pair(0.f, 0.f), none);
+  const float2 no = split(none);
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    if (kTurn) bound = fmaxf(bound, __shfl_xor_sync(0xFFFFFFFFu, bound, o));
+  }
+  const float off = kTurn ? bound * 0x1p-22f : 0.f;  // twice the bound, for the sums below
+  const bool fine = (__ballot_sync(0xFFFFFFFFu, no.x != 0.f || no.y != 0.f) & mask) == 0;
+  const uint32_t zb = bf16_down(lo + off);
+  const float z = __uint_as_float(zb << 16);
+  const float d = hi - z;
+  const float least = (d - off) * (0.06666667f * 0.9999995f), most = (d + off) * (0.06666667f * 1.0000005f);
+  const uint32_t sb = bf16_near(most);
+  if (!fine || (kTurn && bf16_down(lo - off) != zb) || bf16_near(least) != sb || !(most < 1e37f)) {
+    double exact[8];
+    exact_values<kTurn>(a, cs, exact);
+    const uint2 r = quantise_exactly<LANES>(exact, mask);
+    *codes = r.x;
+    *sz = r.y;
+    return;
+  }
+  // (x - z) / s lies within 0 .. 15.03 and what `close` leaves, so the nearest
+  // whole number within 0 .. 15; adding 1.5 * 2^23 leaves it in the low bits, ties
+  // to even.  The upper bits of the eight sums cancel against a constant.
+  const float s = __uint_as_float(sb << 16), inv = s > 0.f ? 1.0f / s : 0.f;
+  const float close = 0.5f - fmaf(off, inv, 4e-6f);  // no closer to a whole number and a half than this
+  const F2 z2 = pair(-z, -z), inv2 = pair(inv, inv), up = pair(12582912.f, 12582912.f),
+           down = pair(-12582912.f, -12582912.f), neg = pair(-1.f, -1.f);
+  uint32_t w = 0u - 0x4B400000u * 0x11111111u;
+  float far = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const F2 t = mul2(add2(pair(x[e], x[e + 1]), z2), inv2), r = add2(t, up);
+    const float2 rs = split(r), f = split(fma2(add2(r, down), neg, t));
+    far = max3(far, fabsf(f.x), fabsf(f.y));
+    w += __float_as_uint(rs.x) << (4 * e);
+    w += __float_as_uint(rs.y) << (4 * e + 4);
+  }
+  const bool sure = far <= close;  // (a NaN of an infinite inv: close is one)
+  if (!sure) {
+    bool held = !kTurn;
+    if (!kTurn) {
+      w = 0;
+      const float half = 0.5f * s;  // s is no denormal number here: inv is finite
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = x[e] - z;
+        held = held && y + z == x[e] && x[e] - y == z;  // nothing was rounded off
+        const float r = fminf(fmaxf(y * inv, 0.f), 15.f) + 12582912.f, rest = fmaf(-(r - 12582912.f), s, y);
+        int c = (int)(__float_as_uint(r) & 15u);
+        const bool odd = c & 1;
+        if (rest > half || (rest == half && odd)) ++c;
+        if (-rest > half || (-rest == half && odd)) --c;
+        w |= (uint32_t)min(max(c, 0), 15) << (4 * e);
+      }
+      held = held && inv < 1e37f;
+    }
+    if (!held) {
+      double exact[8];
+      exact_values<kTurn>(a, cs, exact);
+      w = exact_codes(exact, z, s);
+    }
+  }
+  *codes = w;
+  *sz = sb | zb << 16;
+}
+
+// Bound by bytes: a row comes in once and leaves as HD / 2 + 4 bytes.  H heads of
+// a token a lane.
+template <typename T, int HD, bool kTurn, int H>
+__global__ void __launch_bounds__(kThreadsKv4, 6)
     kv4_append_kernel(const Kv4Dev c, const T* __restrict__ k, int64_t k_tok, int64_t k_head, const T* __restrict__ v,
-                      int64_t v_tok, int64_t v_head, const float* __restrict__ rope) {
+                      int64_t v_tok, int64_t v_head, const float* __restrict__ rope, int groups) {
   constexpr int LANES = HD / 8;
   const int lane = threadIdx.x & 31, j = lane % LANES;
   const uint32_t mask = ((1u << LANES) - 1u) << (lane - j);
   const uint32_t r = blockIdx.x * (kThreadsKv4 / LANES) + threadIdx.x / LANES;
-  const int head = r % (uint32_t)c.n_kv, t = r / (uint32_t)c.n_kv;
-  uint8_t* page;
-  int row, position;
-  locate<LANES>(c, t, head, j, mask, &page, &row, &position);
-  float kx[8] = {}, vx[8] = {};
-  if (page) {
-    const T* kp = k + t * k_tok + head * k_head + 4 * j;
-    const T* vp = v + t * v_tok + head * v_head + 4 * j;
-    load4(kp, kx);
-    load4(kp + HD / 2, kx + 4);
-    load4(vp, vx);
-    load4(vp + HD / 2, vx + 4);
+  const int t = r / (uint32_t)groups, head = (r % (uint32_t)groups) * H, heads = min(H, c.n_kv - head);
+  const T *kp = k + t * k_tok + head * k_head + 4 * j, *vp = v + t * v_tok + head * v_head + 4 * j;
+  float kx[8] = {}, vx[8] = {}, cs[8] = {};
+  auto load = [&](const T* kr, const T* vr) {
+    load4(kr, kx);
+    load4(kr + HD / 2, kx + 4);
+    load4(vr, vx);
+    load4(vr + HD / 2, vx + 4);
+  };
+  if (t < c.total) load(kp, vp);
+  int block, row, position;
+  locate<LANES>(c, t, j, mask, &block, &row, &position);
+  if (kTurn && block >= 0) {
+    const float* a = rope + ((int64_t)position * (HD / 2) + 4 * j) * 2;
+    load4(a, cs);
+    load4(a + 4, cs + 4);
   }
-  uint32_t kw, ksz, vw, vsz;
-  if (rope) {
-    double x[8] = {};
-    if (page) {
-      float cs[8];
-      const float* a = rope + ((int64_t)position * (HD / 2) + 4 * j) * 2;
-      load4(a, cs);
-      load4(a + 4, cs + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const double co = cs[2 * e], si = cs[2 * e + 1], lo = kx[e], hi = kx[4 + e];
-        x[e] = lo * co - hi * si;
-        x[4 + e] = hi * co + lo * si;
-      }
-    }
-    quantise<LANES>(x, mask, &kw, &ksz);
-  } else {
-    quantise<LANES>(kx, mask, &kw, &ksz);
-  }
-  quantise<LANES>(vx, mask, &vw, &vsz);
-  if (!page) return;
   const int codes = c.page_tokens * (HD / 2);
-  *reinterpret_cast<uint32_t*>(page + row * (HD / 2) + 4 * j) = kw;
-  *reinterpret_cast<uint32_t*>(page + codes + row * (HD / 2) + 4 * j) = vw;
-  uint32_t* sz = reinterpret_cast<uint32_t*>(page + 2 * codes) + row;
-  if (j == 0) sz[0] = ksz;
-  if (j == 1) sz[c.page_tokens] = vsz;
+  uint8_t* page = kv4_page(c, max(block, 0), head);
+#pragma unroll 1
+  for (int h = 0; h < H; ++h) {
+    float a[8], b[8];  // this head's; the next one's are asked for
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = kx[e], b[e] = vx[e];
+    if (H > 1 && block >= 0 && h + 1 < heads) load(kp + (h + 1) * k_head, vp + (h + 1) * v_head);
+    uint32_t kw, ksz, vw, vsz;
+    quantise<LANES, false>(b, cs, mask, &vw, &vsz);
+    quantise<LANES, kTurn>(a, cs, mask, &kw, &ksz);
+    if (block >= 0 && h < heads) {
+      *reinterpret_cast<uint32_t*>(page + row * (HD / 2) + 4 * j) = kw;
+      *reinterpret_cast<uint32_t*>(page + codes + row * (HD / 2) + 4 * j) = vw;
+      uint32_t* sz = reinterpret_cast<uint32_t*>(page + 2 * codes) + row;
+      if (j == 0) sz[0] = ksz;
+      if (j == 1) sz[c.page_tokens] = vsz;
+    }
+    page += c.page_bytes;
+  }
 }
 
 template <int HD, typename T>
@@ -195,45 +300,66 @@ __device__ __forceinline__ void read_row(uint32_t w, uint32_t sz, T* out) {
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreadsKv4)
     kv4_read_kernel(const Kv4Dev c, T* __restrict__ k, int64_t k_tok, int64_t k_head, T* __restrict__ v, int64_t v_tok,
-                    int64_t v_head) {
+                    int64_t v_head, int groups) {
   constexpr int LANES = HD / 8;
   const int lane = threadIdx.x & 31, j = lane % LANES;
   const uint32_t mask = ((1u << LANES) - 1u) << (lane - j);
   const uint32_t r = blockIdx.x * (kThreadsKv4 / LANES) + threadIdx.x / LANES;
-  const int head = r % (uint32_t)c.n_kv, t = r / (uint32_t)c.n_kv;
-  uint8_t* page;
-  int row, position;
-  if (!locate<LANES>(c, t, head, j, mask, &page, &row, &position)) return;
-  uint32_t kw = 0, vw = 0, ksz = 0, vsz = 0;
-  if (page) {
-    const int codes = c.page_tokens * (HD / 2);
-    kw = *reinterpret_cast<const uint32_t*>(page + row * (HD / 2) + 4 * j);
-    vw = *reinterpret_cast<const uint32_t*>(page + codes + row * (HD / 2) + 4 * j);
-    const uint32_t* sz = reinterpret_cast<const uint32_t*>(page + 2 * codes) + row;
-    ksz = sz[0];
-    vsz = sz[c.page_tokens];
-  }
-  read_row<HD>(kw, ksz, k + t * k_tok + head * k_head + 4 * j);
-  read_row<HD>(vw, vsz, v + t * v_tok + head * v_head + 4 * j);
+  const int t = r / (uint32_t)groups, head = (r % (uint32_t)groups) * kHeads, heads = min(kHeads, c.n_kv - head);
+  int block, row, position;
+  if (!locate<LANES>(c, t, j, mask, &block, &row, &position)) return;
+  const int codes = c.page_tokens * (HD / 2);
+  uint32_t w[kHeads][4] = {};
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h)
+    if (block >= 0 && h < heads) {
+      const uint8_t* page = kv4_page(c, block, head + h);
+      const uint32_t* sz = reinterpret_cast<const uint32_t*>(page + 2 * codes) + row;
+      w[h][0] = *reinterpret_cast<const uint32_t*>(page + row * (HD / 2) + 4 * j);
+      w[h][1] = *reinterpret_cast<const uint32_t*>(page + codes + row * (HD / 2) + 4 * j);
+      w[h][2] = sz[0];
+      w[h][3] = sz[c.page_tokens];
+    }
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h)
+    if (h < heads) {
+      read_row<HD>(w[h][0], w[h][2], k + t * k_tok + (head + h) * k_head + 4 * j);
+      read_row<HD>(w[h][1], w[h][3], v + t * v_tok + (head + h) * v_head + 4 * j);
+    }
 }
 
 template <int HD>
-uint32_t row_blocks(const Kv4Dev& c) {
+uint32_t row_blocks(const Kv4Dev& c, int groups) {
   constexpr int rows = kThreadsKv4 / (HD / 8);
-  return (uint32_t)(((int64_t)c.total * c.n_kv + rows - 1) / rows);
+  return (uint32_t)(((int64_t)c.total * groups + rows - 1) / rows);
+}
+
+template <typename T, int HD, bool kTurn>
+void launch_append(const Kv4Dev& c, const Kv4Tensor& k, const Kv4Tensor& v, const float* rope, cudaStream_t s) {
+  const T *kp = static_cast<const T*>(k.p), *vp = static_cast<const T*>(v.p);
+  // rows that the GPU holds at once, one a lane group: 148 SMs of 8 CTAs
+  const bool many = (int64_t)c.total * c.n_kv > 148 * 8 * (kThreadsKv4 / (HD / 8)) && c.n_kv > 1;
+  const int groups = many ? (c.n_kv + kHeads - 1) / kHeads : c.n_kv;
+  const uint32_t blocks = row_blocks<HD>(c, groups);
+  if (many)
+    kv4_append_kernel<T, HD, kTurn, kHeads>
+        <<<blocks, kThreadsKv4, 0, s>>>(c, kp, k.token, k.head, vp, v.token, v.head, rope, groups);
+  else
+    kv4_append_kernel<T, HD, kTurn, 1>
+        <<<blocks, kThreadsKv4, 0, s>>>(c, kp, k.token, k.head, vp, v.token, v.head, rope, groups);
 }
 
 template <typename T, int HD>
 void launch_append(const Kv4Dev& c, const Kv4Tensor& k, const Kv4Tensor& v, const float* rope, cudaStream_t s) {
-  kv4_append_kernel<T, HD><<<row_blocks<HD>(c), kThreadsKv4, 0, s>>>(
-      c, static_cast<const T*>(k.p), k.token, k.head, static_cast<const T*>(v.p), v.token, v.head, rope);
+  rope ? launch_append<T, HD, true>(c, k, v, rope, s) : launch_append<T, HD, false>(c, k, v, rope, s);
 }
 
 template <typename T, int HD>
 void launch_read(const Kv4Dev& c, const Kv4Tensor& k, const Kv4Tensor& v, cudaStream_t s) {
-  kv4_read_kernel<T, HD><<<row_blocks<HD>(c), kThreadsKv4, 0, s>>>(
+  const int groups = (c.n_kv + kHeads - 1) / kHeads;
+  kv4_read_kernel<T, HD><<<row_blocks<HD>(c, groups), kThreadsKv4, 0, s>>>(
       c, static_cast<T*>(const_cast<void*>(k.p)), k.token, k.head, static_cast<T*>(const_cast<void*>(v.p)), v.token,
-      v.head);
+      v.head, groups);
 }
 
 int launched(const char* what) {
