@@ -2,10 +2,15 @@
 // way), read back, and the checks of all its entry points.  The attention over
 // it is in kv4_attention.cu.
 //
-// A row of HD values (one token, one kv head, K or V) is handled by HD / 8
-// lanes.  Lane j holds dims 4j .. 4j + 3 and HD / 2 + 4j .. + 3, so that both
-// halves of a rotated pair are in one lane and its eight codes are one 32-bit
-// word of the row.
+// A row of HD values (one token, one kv head, K or V) is handled by HD / 16
+// lanes.  Lane j holds dims 8j .. 8j + 7 and HD / 2 + 8j .. + 7, so that both
+// halves of a rotated pair are in one lane and its sixteen codes are two 32-bit
+// words of the row.  A CTA takes consecutive tokens of one head: their rows are
+// neighbours in a page.
+//
+// A row's place takes some loads that wait for one another (the search for its
+// sequence, the position, the page id, the angles), 2 us or so; the append's rows
+// are under way before their place is known.
 #include <limits.h>
 
 #include "kv4.cuh"
@@ -16,7 +21,7 @@ namespace wpk {
 namespace {
 
 constexpr int kThreadsKv4 = 128;
-constexpr int kHeads = 4;  // heads of a token that lanes take together
+constexpr int kOf = 16;  // values of a row that a lane holds
 
 // Sequence of token t: the last b with indptr[b] <= t, searched by the LANES
 // lanes of a row together (each round they probe LANES evenly spaced starts,
@@ -56,7 +61,7 @@ __device__ __forceinline__ bool locate(const Kv4Dev& c, int t, int j, uint32_t m
   const int first = c.pos[b];
   const int64_t p = (int64_t)first + (t - q0);
   if (first < 0 || p >= (int64_t)c.max_blocks * c.page_tokens || p >= c.rope_positions) return true;
-  const int slot = (int)p / c.page_tokens;
+  const int slot = kv4_slot(c, (int)p);
   const int id = c.table[(int64_t)b * c.max_blocks + slot];
   if (id < 0 || id >= c.n_blocks) return true;
   *block = id;
@@ -82,38 +87,36 @@ __device__ __forceinline__ uint32_t bf16_near(double x) {
 }
 
 // Codes of the lane's values from exact ones.
-__device__ __forceinline__ uint32_t exact_codes(const double (&x)[8], float z, float s) {
-  uint32_t w = 0;
+__device__ __noinline__ uint2 exact_codes(const double* x, float z, float s) {
+  uint32_t w[2] = {0, 0};
 #pragma unroll 1
-  for (int e = 0; e < 8; ++e) {
-    double v = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v = i == e ? x[i] : v;  // registers have no index
-    const double c = s > 0.f ? rint((v - (double)z) / (double)s) : 0.0;
-    w |= (uint32_t)fmin(fmax(c, 0.0), 15.0) << (4 * e);
+  for (int e = 0; e < kOf; ++e) {
+    const double c = s > 0.f ? rint((x[e] - (double)z) / (double)s) : 0.0;
+    const uint32_t n = (uint32_t)fmin(fmax(c, 0.0), 15.0);
+    // value e is the (e % 4)-th of its half of word (e / 4) % 2
+    w[(e >> 2) & 1] |= n << (4 * ((e & 3) + (e >= kOf / 2 ? 4 : 0)));
   }
-  return w;
+  return make_uint2(w[0], w[1]);
 }
 
 // The lane's values in 64 bits: turned (each product is exact, the sum rounds
 // once), or as they are.
 template <bool kTurn>
-__device__ __forceinline__ void exact_values(const float (&a)[8], const float (&cs)[8], double (&x)[8]) {
+__device__ __forceinline__ void exact_values(const float (&a)[kOf], const float (&cs)[kOf], double* x) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const double lo = a[e], hi = a[4 + e];
+  for (int e = 0; e < kOf / 2; ++e) {
+    const double lo = a[e], hi = a[kOf / 2 + e];
     x[e] = kTurn ? lo * cs[2 * e] - hi * cs[2 * e + 1] : lo;
-    x[4 + e] = kTurn ? hi * cs[2 * e] + lo * cs[2 * e + 1] : hi;
+    x[kOf / 2 + e] = kTurn ? hi * cs[2 * e] + lo * cs[2 * e + 1] : hi;
   }
 }
 
 // A row in 64 bits throughout.
 template <int LANES>
-__device__ __noinline__ uint2 quantise_exactly(const double (&x)[8], uint32_t mask) {
+__device__ __noinline__ uint3 quantise_exactly(const double* x, uint32_t mask) {
   double lo = x[0], hi = x[0];
   bool fine = true;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < kOf; ++e) {
     lo = fmin(lo, x[e]);
     hi = fmax(hi, x[e]);
     fine = fine && isfinite(x[e]);
@@ -123,14 +126,15 @@ __device__ __noinline__ uint2 quantise_exactly(const double (&x)[8], uint32_t ma
     lo = fmin(lo, __shfl_xor_sync(mask, lo, o));
     hi = fmax(hi, __shfl_xor_sync(mask, hi, o));
   }
-  if (__ballot_sync(mask, !fine) & mask) return make_uint2(0u, 0x7FC00000u);  // s = 0, z = NaN: reads as NaN
+  if (__ballot_sync(mask, !fine) & mask) return make_uint3(0u, 0u, 0x7FC00000u);  // s = 0, z = NaN: reads as NaN
   const uint32_t zb = bf16_down(__double2float_rd(lo));
   const float z = __uint_as_float(zb << 16);
   const uint32_t sb = bf16_near((hi - (double)z) / 15.0);
-  return make_uint2(exact_codes(x, z, __uint_as_float(sb << 16)), sb | zb << 16);
+  const uint2 w = exact_codes(x, z, __uint_as_float(sb << 16));
+  return make_uint3(w.x, w.y, sb | zb << 16);
 }
 
-// Eight codes of this lane and the row's (s, z) word, those of exact arithmetic.
+// Sixteen codes of this lane and the row's (s, z) word, those of exact arithmetic.
 // The work is done in 32 bits with bounds: a turned value is off by at most 2^-23
 // of |a cos| + |b sin| (a product and a sum round), which 2 max |a| max |cos, sin|
 // bounds.  Where z or s could be
@@ -141,34 +145,40 @@ __device__ __noinline__ uint2 quantise_exactly(const double (&x)[8], uint32_t ma
 // from z and s have few digits - and there the remainder x - z - c s decides,
 // which 32 bits hold exactly where they hold x - z.
 template <int LANES, bool kTurn>
-__device__ __forceinline__ void quantise(const float (&a)[8], const float (&cs)[8], uint32_t mask, uint32_t* codes,
-                                         uint32_t* sz) {
-  float x[8], bound = 0.f;
+__device__ __forceinline__ uint3 quantise(const float (&a)[kOf], const float (&cs)[kOf], uint32_t mask) {
+  constexpr int HALF = kOf / 2;
+  float x[kOf], bound = 0.f;
   if (kTurn) {
-    float am = max3(fabsf(a[0]), fabsf(a[1]), fabsf(a[2])), cm = max3(fabsf(cs[0]), fabsf(cs[1]), fabsf(cs[2]));
-    am = max3(max3(am, fabsf(a[3]), fabsf(a[4])), fabsf(a[5]), fmaxf(fabsf(a[6]), fabsf(a[7])));
-    cm = max3(max3(cm, fabsf(cs[3]), fabsf(cs[4])), fabsf(cs[5]), fmaxf(fabsf(cs[6]), fabsf(cs[7])));
+    float am = 0.f, cm = 0.f;
+#pragma unroll
+    for (int e = 0; e < kOf; e += 2) {
+      am = max3(am, fabsf(a[e]), fabsf(a[e + 1]));
+      cm = max3(cm, fabsf(cs[e]), fabsf(cs[e + 1]));
+    }
     bound = 2.f * am * cm;
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const F2 lo = pair(a[e], a[e + 1]), hi = pair(a[4 + e], a[5 + e]);
+    for (int e = 0; e < HALF; e += 2) {
+      const F2 lo = pair(a[e], a[e + 1]), hi = pair(a[HALF + e], a[HALF + e + 1]);
       const F2 co = pair(cs[2 * e], cs[2 * e + 2]), si = pair(cs[2 * e + 1], cs[2 * e + 3]);
       const F2 minus = pair(-cs[2 * e + 1], -cs[2 * e + 3]);
       const float2 r = split(fma2(lo, co, mul2(hi, minus))), q = split(fma2(hi, co, mul2(lo, si)));
       x[e] = r.x;
       x[e + 1] = r.y;
-      x[4 + e] = q.x;
-      x[5 + e] = q.y;
+      x[HALF + e] = q.x;
+      x[HALF + e + 1] = q.y;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = a[e];
+    for (int e = 0; e < kOf; ++e) x[e] = a[e];
   }
-  float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), fminf(x[6], x[7]));
-  float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+  float lo = x[0], hi = x[0];
   F2 none = pair(0.f, 0.f);  // a NaN where any value is one, or infinite
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) none = fma2(pair(x[e], x[e + 1]), pair(0.f, 0.f), none);
+  for (int e = 0; e < kOf; e += 2) {
+    lo = min3(lo, x[e], x[e + 1]);
+    hi = max3(hi, x[e], x[e + 1]);
+    none = fma2(pair(x[e], x[e + 1]), pair(0.f, 0.f), none);
+  }
   const float2 no = split(none);
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) {
@@ -184,110 +194,100 @@ __device__ __forceinline__ void quantise(const float (&a)[8], const float (&cs)[
   const float least = (d - off) * (0.06666667f * 0.9999995f), most = (d + off) * (0.06666667f * 1.0000005f);
   const uint32_t sb = bf16_near(most);
   if (!fine || (kTurn && bf16_down(lo - off) != zb) || bf16_near(least) != sb || !(most < 1e37f)) {
-    double exact[8];
+    double exact[kOf];
     exact_values<kTurn>(a, cs, exact);
-    const uint2 r = quantise_exactly<LANES>(exact, mask);
-    *codes = r.x;
-    *sz = r.y;
-    return;
+    return quantise_exactly<LANES>(exact, mask);
   }
   // (x - z) / s lies within 0 .. 15.03 and what `close` leaves, so the nearest
   // whole number within 0 .. 15; adding 1.5 * 2^23 leaves it in the low bits, ties
-  // to even.  The upper bits of the eight sums cancel against a constant.
+  // to even.  The upper bits of a word's eight sums cancel against a constant.
   const float s = __uint_as_float(sb << 16), inv = s > 0.f ? 1.0f / s : 0.f;
   const float close = 0.5f - fmaf(off, inv, 4e-6f);  // no closer to a whole number and a half than this
   const F2 z2 = pair(-z, -z), inv2 = pair(inv, inv), up = pair(12582912.f, 12582912.f),
            down = pair(-12582912.f, -12582912.f), neg = pair(-1.f, -1.f);
-  uint32_t w = 0u - 0x4B400000u * 0x11111111u;
+  uint32_t w[2] = {0u - 0x4B400000u * 0x11111111u, 0u - 0x4B400000u * 0x11111111u};
   float far = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
+  for (int e = 0; e < kOf; e += 2) {
     const F2 t = mul2(add2(pair(x[e], x[e + 1]), z2), inv2), r = add2(t, up);
     const float2 rs = split(r), f = split(fma2(add2(r, down), neg, t));
     far = max3(far, fabsf(f.x), fabsf(f.y));
-    w += __float_as_uint(rs.x) << (4 * e);
-    w += __float_as_uint(rs.y) << (4 * e + 4);
+    const int at = 4 * ((e & 3) + (e >= HALF ? 4 : 0));
+    w[(e >> 2) & 1] += (__float_as_uint(rs.x) << at) + (__float_as_uint(rs.y) << (at + 4));
   }
-  const bool sure = far <= close;  // (a NaN of an infinite inv: close is one)
-  if (!sure) {
-    bool held = !kTurn;
+  if (!(far <= close)) {  // (a NaN of an infinite inv: close is one)
+    bool held = !kTurn && inv < 1e37f;
     if (!kTurn) {
-      w = 0;
+      w[0] = w[1] = 0;
       const float half = 0.5f * s;  // s is no denormal number here: inv is finite
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < kOf; ++e) {
         const float y = x[e] - z;
         held = held && y + z == x[e] && x[e] - y == z;  // nothing was rounded off
-        const float r = fminf(fmaxf(y * inv, 0.f), 15.f) + 12582912.f, rest = fmaf(-(r - 12582912.f), s, y);
+        const float r = y * inv + 12582912.f, rest = fmaf(-(r - 12582912.f), s, y);
         int c = (int)(__float_as_uint(r) & 15u);
-        const bool odd = c & 1;
-        if (rest > half || (rest == half && odd)) ++c;
-        if (-rest > half || (-rest == half && odd)) --c;
-        w |= (uint32_t)min(max(c, 0), 15) << (4 * e);
+        if (rest > half || (rest == half && (c & 1))) ++c;
+        if (-rest > half || (-rest == half && (c & 1))) --c;
+        w[(e >> 2) & 1] |= (uint32_t)c << (4 * ((e & 3) + (e >= HALF ? 4 : 0)));
       }
-      held = held && inv < 1e37f;
     }
     if (!held) {
-      double exact[8];
+      double exact[kOf];
       exact_values<kTurn>(a, cs, exact);
-      w = exact_codes(exact, z, s);
+      const uint2 r = exact_codes(exact, z, s);
+      w[0] = r.x;
+      w[1] = r.y;
     }
   }
-  *codes = w;
-  *sz = sb | zb << 16;
+  return make_uint3(w[0], w[1], sb | zb << 16);
 }
 
-// Bound by bytes: a row comes in once and leaves as HD / 2 + 4 bytes.  H heads of
-// a token a lane.
-template <typename T, int HD, bool kTurn, int H>
-__global__ void __launch_bounds__(kThreadsKv4, 6)
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  load4(p, f);
+  load4(p + 4, f + 4);
+}
+
+// Bound by bytes: a row comes in once and leaves as HD / 2 + 4 bytes.
+template <typename T, int HD, bool kTurn>
+__global__ void __launch_bounds__(kThreadsKv4, kTurn ? 7 : 8)
     kv4_append_kernel(const Kv4Dev c, const T* __restrict__ k, int64_t k_tok, int64_t k_head, const T* __restrict__ v,
-                      int64_t v_tok, int64_t v_head, const float* __restrict__ rope, int groups) {
-  constexpr int LANES = HD / 8;
-  const int lane = threadIdx.x & 31, j = lane % LANES;
+                      int64_t v_tok, int64_t v_head, const float* __restrict__ rope) {
+  constexpr int LANES = HD / kOf;
+  const int lane = threadIdx.x & 31, j = lane % LANES, head = blockIdx.y;
   const uint32_t mask = ((1u << LANES) - 1u) << (lane - j);
-  const uint32_t r = blockIdx.x * (kThreadsKv4 / LANES) + threadIdx.x / LANES;
-  const int t = r / (uint32_t)groups, head = (r % (uint32_t)groups) * H, heads = min(H, c.n_kv - head);
-  const T *kp = k + t * k_tok + head * k_head + 4 * j, *vp = v + t * v_tok + head * v_head + 4 * j;
-  float kx[8] = {}, vx[8] = {}, cs[8] = {};
-  auto load = [&](const T* kr, const T* vr) {
-    load4(kr, kx);
-    load4(kr + HD / 2, kx + 4);
-    load4(vr, vx);
-    load4(vr + HD / 2, vx + 4);
-  };
-  if (t < c.total) load(kp, vp);
+  const int t = blockIdx.x * (kThreadsKv4 / LANES) + threadIdx.x / LANES;
+  float kx[kOf] = {}, vx[kOf] = {}, cs[kOf] = {};
+  if (t < c.total) {
+    const T* kp = k + t * k_tok + head * k_head + 8 * j;
+    const T* vp = v + t * v_tok + head * v_head + 8 * j;
+    load8(vp, vx);
+    load8(vp + HD / 2, vx + 8);
+    load8(kp, kx);
+    load8(kp + HD / 2, kx + 8);
+  }
   int block, row, position;
   locate<LANES>(c, t, j, mask, &block, &row, &position);
   if (kTurn && block >= 0) {
-    const float* a = rope + ((int64_t)position * (HD / 2) + 4 * j) * 2;
-    load4(a, cs);
-    load4(a + 4, cs + 4);
+    const float* a = rope + ((int64_t)position * (HD / 2) + 8 * j) * 2;
+    load8(a, cs);
+    load8(a + 8, cs + 8);
   }
+  const uint3 vq = quantise<LANES, false>(vx, cs, mask);
+  const uint3 kq = quantise<LANES, kTurn>(kx, cs, mask);
+  if (block < 0) return;
+  uint8_t* page = kv4_page(c, block, head);
   const int codes = c.page_tokens * (HD / 2);
-  uint8_t* page = kv4_page(c, max(block, 0), head);
-#pragma unroll 1
-  for (int h = 0; h < H; ++h) {
-    float a[8], b[8];  // this head's; the next one's are asked for
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = kx[e], b[e] = vx[e];
-    if (H > 1 && block >= 0 && h + 1 < heads) load(kp + (h + 1) * k_head, vp + (h + 1) * v_head);
-    uint32_t kw, ksz, vw, vsz;
-    quantise<LANES, false>(b, cs, mask, &vw, &vsz);
-    quantise<LANES, kTurn>(a, cs, mask, &kw, &ksz);
-    if (block >= 0 && h < heads) {
-      *reinterpret_cast<uint32_t*>(page + row * (HD / 2) + 4 * j) = kw;
-      *reinterpret_cast<uint32_t*>(page + codes + row * (HD / 2) + 4 * j) = vw;
-      uint32_t* sz = reinterpret_cast<uint32_t*>(page + 2 * codes) + row;
-      if (j == 0) sz[0] = ksz;
-      if (j == 1) sz[c.page_tokens] = vsz;
-    }
-    page += c.page_bytes;
-  }
+  *reinterpret_cast<uint2*>(page + row * (HD / 2) + 8 * j) = make_uint2(kq.x, kq.y);
+  *reinterpret_cast<uint2*>(page + codes + row * (HD / 2) + 8 * j) = make_uint2(vq.x, vq.y);
+  uint32_t* sz = reinterpret_cast<uint32_t*>(page + 2 * codes) + row;
+  if (j == 0) sz[0] = kq.z;
+  if (j == 1) sz[c.page_tokens] = vq.z;
 }
 
+// A word of a row's codes as values, to dims 4w and HD / 2 + 4w of it.
 template <int HD, typename T>
-__device__ __forceinline__ void read_row(uint32_t w, uint32_t sz, T* out) {
+__device__ __forceinline__ void read_word(uint32_t w, uint32_t sz, T* out) {
   const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xFFFF0000u);
   float x[8];
 #pragma unroll
@@ -300,66 +300,53 @@ __device__ __forceinline__ void read_row(uint32_t w, uint32_t sz, T* out) {
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreadsKv4)
     kv4_read_kernel(const Kv4Dev c, T* __restrict__ k, int64_t k_tok, int64_t k_head, T* __restrict__ v, int64_t v_tok,
-                    int64_t v_head, int groups) {
-  constexpr int LANES = HD / 8;
-  const int lane = threadIdx.x & 31, j = lane % LANES;
+                    int64_t v_head) {
+  constexpr int LANES = HD / kOf;
+  const int lane = threadIdx.x & 31, j = lane % LANES, head = blockIdx.y;
   const uint32_t mask = ((1u << LANES) - 1u) << (lane - j);
-  const uint32_t r = blockIdx.x * (kThreadsKv4 / LANES) + threadIdx.x / LANES;
-  const int t = r / (uint32_t)groups, head = (r % (uint32_t)groups) * kHeads, heads = min(kHeads, c.n_kv - head);
+  const int t = blockIdx.x * (kThreadsKv4 / LANES) + threadIdx.x / LANES;
   int block, row, position;
   if (!locate<LANES>(c, t, j, mask, &block, &row, &position)) return;
-  const int codes = c.page_tokens * (HD / 2);
-  uint32_t w[kHeads][4] = {};
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h)
-    if (block >= 0 && h < heads) {
-      const uint8_t* page = kv4_page(c, block, head + h);
-      const uint32_t* sz = reinterpret_cast<const uint32_t*>(page + 2 * codes) + row;
-      w[h][0] = *reinterpret_cast<const uint32_t*>(page + row * (HD / 2) + 4 * j);
-      w[h][1] = *reinterpret_cast<const uint32_t*>(page + codes + row * (HD / 2) + 4 * j);
-      w[h][2] = sz[0];
-      w[h][3] = sz[c.page_tokens];
-    }
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h)
-    if (h < heads) {
-      read_row<HD>(w[h][0], w[h][2], k + t * k_tok + (head + h) * k_head + 4 * j);
-      read_row<HD>(w[h][1], w[h][3], v + t * v_tok + (head + h) * v_head + 4 * j);
-    }
+  uint2 kw = make_uint2(0, 0), vw = kw;
+  uint32_t ksz = 0, vsz = 0;
+  if (block >= 0) {
+    const int codes = c.page_tokens * (HD / 2);
+    const uint8_t* page = kv4_page(c, block, head);
+    const uint32_t* sz = reinterpret_cast<const uint32_t*>(page + 2 * codes) + row;
+    kw = *reinterpret_cast<const uint2*>(page + row * (HD / 2) + 8 * j);
+    vw = *reinterpret_cast<const uint2*>(page + codes + row * (HD / 2) + 8 * j);
+    ksz = sz[0];
+    vsz = sz[c.page_tokens];
+  }
+  T *kp = k + t * k_tok + head * k_head + 8 * j, *vp = v + t * v_tok + head * v_head + 8 * j;
+  read_word<HD>(kw.x, ksz, kp);
+  read_word<HD>(kw.y, ksz, kp + 4);
+  read_word<HD>(vw.x, vsz, vp);
+  read_word<HD>(vw.y, vsz, vp + 4);
 }
 
 template <int HD>
-uint32_t row_blocks(const Kv4Dev& c, int groups) {
-  constexpr int rows = kThreadsKv4 / (HD / 8);
-  return (uint32_t)(((int64_t)c.total * groups + rows - 1) / rows);
-}
-
-template <typename T, int HD, bool kTurn>
-void launch_append(const Kv4Dev& c, const Kv4Tensor& k, const Kv4Tensor& v, const float* rope, cudaStream_t s) {
-  const T *kp = static_cast<const T*>(k.p), *vp = static_cast<const T*>(v.p);
-  // rows that the GPU holds at once, one a lane group: 148 SMs of 8 CTAs
-  const bool many = (int64_t)c.total * c.n_kv > 148 * 8 * (kThreadsKv4 / (HD / 8)) && c.n_kv > 1;
-  const int groups = many ? (c.n_kv + kHeads - 1) / kHeads : c.n_kv;
-  const uint32_t blocks = row_blocks<HD>(c, groups);
-  if (many)
-    kv4_append_kernel<T, HD, kTurn, kHeads>
-        <<<blocks, kThreadsKv4, 0, s>>>(c, kp, k.token, k.head, vp, v.token, v.head, rope, groups);
-  else
-    kv4_append_kernel<T, HD, kTurn, 1>
-        <<<blocks, kThreadsKv4, 0, s>>>(c, kp, k.token, k.head, vp, v.token, v.head, rope, groups);
+dim3 row_blocks(const Kv4Dev& c) {
+  constexpr int tokens = kThreadsKv4 / (HD / kOf);
+  return dim3((unsigned)((c.total + tokens - 1) / tokens), (unsigned)c.n_kv);
 }
 
 template <typename T, int HD>
 void launch_append(const Kv4Dev& c, const Kv4Tensor& k, const Kv4Tensor& v, const float* rope, cudaStream_t s) {
-  rope ? launch_append<T, HD, true>(c, k, v, rope, s) : launch_append<T, HD, false>(c, k, v, rope, s);
+  const T *kp = static_cast<const T*>(k.p), *vp = static_cast<const T*>(v.p);
+  if (rope)
+    kv4_append_kernel<T, HD, true>
+        <<<row_blocks<HD>(c), kThreadsKv4, 0, s>>>(c, kp, k.token, k.head, vp, v.token, v.head, rope);
+  else
+    kv4_append_kernel<T, HD, false>
+        <<<row_blocks<HD>(c), kThreadsKv4, 0, s>>>(c, kp, k.token, k.head, vp, v.token, v.head, rope);
 }
 
 template <typename T, int HD>
 void launch_read(const Kv4Dev& c, const Kv4Tensor& k, const Kv4Tensor& v, cudaStream_t s) {
-  const int groups = (c.n_kv + kHeads - 1) / kHeads;
-  kv4_read_kernel<T, HD><<<row_blocks<HD>(c, groups), kThreadsKv4, 0, s>>>(
+  kv4_read_kernel<T, HD><<<row_blocks<HD>(c), kThreadsKv4, 0, s>>>(
       c, static_cast<T*>(const_cast<void*>(k.p)), k.token, k.head, static_cast<T*>(const_cast<void*>(v.p)), v.token,
-      v.head, groups);
+      v.head);
 }
 
 int launched(const char* what) {
@@ -398,6 +385,7 @@ int kv4_view(const wpk_kv4_cache* cache, const int32_t* pos, const int32_t* indp
     return op_fail(WPK_ERR_SHAPE, "a sequence of more than 2^31 - 1 positions");
   if (dtype != WPK_F32 && dtype != WPK_BF16 && dtype != WPK_F16) return op_fail(WPK_ERR_INVALID_ARG, "bad dtype");
   if (total < 0) return op_fail(WPK_ERR_INVALID_ARG, "total must be >= 0");
+  if (cache->n_kv_heads > 65535) return op_fail(WPK_ERR_SHAPE, "more than 65535 kv heads");
   if ((int64_t)total * cache->n_kv_heads > INT_MAX) return op_fail(WPK_ERR_SHAPE, "more than 2^31 - 1 rows");
   if (!indptr && total % cache->batch)
     return op_fail(WPK_ERR_SHAPE, "without indptr, total must be a multiple of the batch");
@@ -411,6 +399,7 @@ int kv4_view(const wpk_kv4_cache* cache, const int32_t* pos, const int32_t* indp
   d->n_kv = cache->n_kv_heads;
   d->page_tokens = cache->page_tokens;
   d->page_bytes = (int)bytes;
+  d->page_magic = ((1ull << 39) + cache->page_tokens - 1) / cache->page_tokens;
   d->pos = pos;
   d->indptr = indptr;
   d->n_seq = nullptr;

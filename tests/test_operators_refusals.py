@@ -77,7 +77,8 @@ def test_cache_calls(name):
     _refused(ARGS, lambda: call(_cache(), dt=3), "dtype")
     _refused(ARGS, lambda: call(_cache(), total=-2), "total")
     _refused(SHAPE, lambda: call(_cache(), total=3), "multiple")
-    _refused(SHAPE, lambda: call(_cache(n_kv_heads=1 << 20), total=1 << 12), "rows")
+    _refused(SHAPE, lambda: call(_cache(n_kv_heads=1 << 15), total=1 << 17), "rows")
+    _refused(SHAPE, lambda: call(_cache(n_kv_heads=1 << 16)), "kv heads")
     for st in ((130, 64), (128, 66), (-128, 64), (128, -64)):
         _refused(ARGS, lambda: call(_cache(), st=st), "strides")
 
