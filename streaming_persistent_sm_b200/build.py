@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwpk.so")
 TORCH_LIB = os.path.join(HERE, "_wpk_torch.so")
 SOURCES = ["graph.cpp", "planner.cpp", "runtime.cu", "capi.cu", "noalloc.cu", "debug_gemm.cu", "kv4.cu",
-           "kv4_attention.cu", "sample.cu"]
+           "kv4_attention.cu", "kv4_prefill.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

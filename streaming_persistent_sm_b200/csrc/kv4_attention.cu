@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "kv4.cuh"
+#include "kv4_codes.cuh"
 #include "kv4_host.h"
 #include "op_util.cuh"
 #include "ptx.cuh"
@@ -43,6 +44,7 @@ namespace {
 constexpr int kRows = 8;    // query rows of a CTA (the N of the P V product)
 constexpr int kKeys = 64;   // keys of a warp's step
 constexpr int kMaxSplit = 16;
+constexpr int kManyRows = 48;  // of a (sequence, kv head): the tcgen05 kernel's from here on
 
 // A CTA of WARPS warps: 4, of which an SM holds four (three at head_dim 128), or
 // 12, one to an SM, where 16 CTAs a cluster would not fill the GPU otherwise.
@@ -68,29 +70,6 @@ struct AttnArgs {
   float scale_log2;                       // scale * log2(e)
 };
 
-__device__ __forceinline__ void cp16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-
 // d += a b: a 16 x 16 (fp16, rows), b 16 x 8 (fp16, columns), d fp32.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -98,31 +77,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;
-
-// The codes less 8 of two even nibbles, and of two odd ones times 16.
-__device__ __forceinline__ uint32_t centred_even(uint32_t w) {
-  const uint32_t u = (w & kEven) | 0x64006400u, eight = 0x64086408u;  // 1032
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&eight));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-__device__ __forceinline__ uint32_t centred_odd(uint32_t w) {
-  const uint32_t u = (w & kOdd) | 0x64006400u, eight = 0x64806480u;  // 1024 + 16 * 8
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&eight));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-
-// What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's
-// codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
-// that the output's rounding is off, relative, of random values).  fp16: Q to 22
-// bits, V centred.  fp32: K centred and P to 22 bits too, and a step's own sums,
-// since the tensor pipe cuts off what its sums cannot hold.
-template <typename T>
-struct Keep {
-  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value, kFp32 = std::is_same<T, float>::value;
-  static constexpr bool kQLow = !kBf16, kPLow = kFp32, kCentreK = kFp32, kCentreV = !kBf16, kOwnSums = kBf16 || kFp32;
-};
 
 // In a warp, lane = 4 g + t.  S's columns 2t and 2t + 1 of the n-th group of 8
 // keys are its keys t and 7 - t: with this order neither the K rows (8 at a
@@ -665,7 +619,9 @@ int kv4_attention_launch(const Kv4Dev& d, int head_dim, int max_new, const Kv4Te
   a.row_blocks = (int)row_blocks;
   cudaError_t e;
   const bool wide = head_dim == 128;
-  if (dtype == WPK_F32)
+  if ((int64_t)a.max_new * a.group >= kManyRows)
+    e = kv4_prefill_launch(d, head_dim, a.max_new, q, a.group, dtype, rope, a.scale_log2, out, s);
+  else if (dtype == WPK_F32)
     e = wide ? choose<float, 128>(d, q, out, a, items, s) : choose<float, 64>(d, q, out, a, items, s);
   else if (dtype == WPK_BF16)
     e = wide ? choose<__nv_bfloat16, 128>(d, q, out, a, items, s) : choose<__nv_bfloat16, 64>(d, q, out, a, items, s);

@@ -1,0 +1,68 @@
+// What the attention kernels over a 4-bit cache share: copies, codes as fp16
+// operands, and what each type keeps.
+#pragma once
+#include <type_traits>
+
+#include "op_util.cuh"
+#include "ptx.cuh"
+
+namespace wpk {
+
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;
+
+// The codes less 8 of two even nibbles, and of two odd ones times 16.
+__device__ __forceinline__ uint32_t centred_even(uint32_t w) {
+  const uint32_t u = (w & kEven) | 0x64006400u, eight = 0x64086408u;  // 1032
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&eight));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t centred_odd(uint32_t w) {
+  const uint32_t u = (w & kOdd) | 0x64006400u, eight = 0x64806480u;  // 1024 + 16 * 8
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&eight));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <bool kCentre>
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
+  return kCentre ? centred_even(w) : w & kEven;
+}
+template <bool kCentre>
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
+  return kCentre ? centred_odd(w) : w & kOdd;
+}
+
+// What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's
+// codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
+// that the output's rounding is off, relative, of random values).  fp16: Q to 22
+// bits, V centred.  fp32: K centred and P to 22 bits too, and a step's own sums,
+// since the tensor pipe cuts off what its sums cannot hold.
+template <typename T>
+struct Keep {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value, kFp32 = std::is_same<T, float>::value;
+  static constexpr bool kQLow = !kBf16, kPLow = kFp32, kCentreK = kFp32, kCentreV = !kBf16, kOwnSums = kBf16 || kFp32;
+};
+
+}  // namespace wpk
