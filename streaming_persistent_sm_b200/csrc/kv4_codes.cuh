@@ -33,15 +33,17 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t u) {
 
 constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;
 
-// The codes less 8 of two even nibbles, and of two odd ones times 16.
+// The codes less kLess of two even nibbles, and of two odd ones times 16.
+template <int kLess = 8>
 __device__ __forceinline__ uint32_t centred_even(uint32_t w) {
-  const uint32_t u = (w & kEven) | 0x64006400u, eight = 0x64086408u;  // 1032
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&eight));
+  const uint32_t u = (w & kEven) | 0x64006400u, less = (0x6400u + kLess) * 0x10001u;  // 1024 + kLess
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&less));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
+template <int kLess = 8>
 __device__ __forceinline__ uint32_t centred_odd(uint32_t w) {
-  const uint32_t u = (w & kOdd) | 0x64006400u, eight = 0x64806480u;  // 1024 + 16 * 8
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&eight));
+  const uint32_t u = (w & kOdd) | 0x64006400u, less = (0x6400u + 16 * kLess) * 0x10001u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&less));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 

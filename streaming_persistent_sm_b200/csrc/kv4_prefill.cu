@@ -1,19 +1,24 @@
 // Attention over a paged KV cache held in 4 bits, for many query rows per kv
 // head (runs of new tokens): 128 rows a CTA on tcgen05.
 //
-// As for few rows (kv4_attention.cu), the products run on the codes: a code is
-// an fp16 after one AND, scales and offsets enter per key around the products.
-// A tile of 64 keys is expanded to operands in shared memory once for all 128
-// rows: K's rows as they are (word j of a row's codes is unit j; Q's dims are put
-// in the same order, odd nibbles' factor 16 taken off them), V transposed (a
-// thread takes the same nibbles of eight keys).  S = Q K^T goes to TMEM; two
-// threads a row (32 keys each) turn it into P, in TMEM too, which is the first
-// operand of O = P V^T; O of a tile is added to the row's registers, rounded.
+// A tile of 64 keys is expanded to fp16 operands in shared memory once for all
+// 128 rows, K and V alike: a key's row of 128 bytes (64 dims), word j of its codes
+// as 16 bytes j, so that Q's dims and the output's stand in the same order (4j,
+// HD/2 + 4j, 4j + 1, ...).  For S = Q K^T K is K-major, for O = P V the same layout
+// of V is MN-major: nothing is transposed.  What the operands hold depends on what
+// the type has to keep:
+//  * bf16: the values s c + z rounded to fp16 (2^-12, as Q and P), times a power of
+//    two that follows the largest value so far;
+//  * fp16, fp32: the codes, which are exact (odd nibbles at 16 times their value);
+//    scales and offsets enter per key around the products, as for few rows.
+// S goes to TMEM; two threads a row (32 keys each) turn it into P, in TMEM too,
+// which is the first operand of O = P V; the O of a tile is added to the row's
+// registers, rounded.
 //
-// Bound by exp2 and the arithmetic around it (16 keys x 128 rows take an SM 128
-// cycles of exp2 alone, the two products of 64 keys some 250 at heads of 64).
-// While a tile's O is computed the next one is expanded, and two CTAs or more
-// share an SM.  Splits of the keys over a cluster join as for few rows.
+// Bound by the arithmetic around the products: for a tile the 128 rows' exp2
+// alone take an SM 512 cycles, the products of heads of 64 some 250.  While a
+// tile's O is computed the next one is expanded, and two CTAs share an SM.
+// Splits of the keys over a cluster join as for few rows.
 #include <limits.h>
 #include <math.h>
 
@@ -43,10 +48,8 @@ struct PGeo {
   static constexpr int kKBytes = kTile * HD * 2, kVBytes = HD * kTile * 2;
   static constexpr int kQ = 0, kQl = kQ + kQBytes, kK = kQl + (P::kQLow ? kQBytes : 0), kV = kK + 2 * kKBytes;
   static constexpr int kOps = kV + 2 * kVBytes;               // operands: 1024-byte aligned
-  // staging: K's codes, V's (16 bytes more every 8 keys, so that a word of eight
-  // keys is read from different banks), the scales
-  static constexpr int kVStage = kTile * HD / 2 + kTile / 8 * 16;
-  static constexpr int kStage = kTile * HD / 2 + kVStage + kTile * 8;
+  static constexpr int kCodes = kTile * HD / 2;               // staging: K's codes, V's, the scales
+  static constexpr int kStage = 2 * kCodes + kTile * 8;
   static constexpr int kScales = kOps + 2 * kStage;           // the tile's scales as floats
   static constexpr int kRed = kScales + kTile * 16;           // [2][kM] floats: both threads of a row
   static constexpr int kBytes = kRed + 2 * kM * 4;
@@ -55,6 +58,7 @@ struct PGeo {
   static constexpr int kSmem = (kBytes > kJoin ? kBytes : kJoin) + 1024;  // and what aligns it
   static constexpr int kS = 0, kO = 64, kCols = HD == 64 ? 128 : 256;  // TMEM: S (P over it), O
   static constexpr int kPerSm = HD == 64 ? 2 : 1;
+  static constexpr bool kValues = P::kBf16;                   // operands hold values, not codes
 };
 
 struct PrefillArgs {
@@ -138,11 +142,11 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       const int key = tile * kTile + p_key, row = key - kv4_slot(c, key) * c.page_tokens;
       const uint8_t* src = kv4_page(c, block, head) + row * (HD / 2) + p_at;
       cp16(stage + p_key * (HD / 2) + p_at, src);
-      cp16(stage + kTile * HD / 2 + p_key * (HD / 2) + (p_key >> 3) * 16 + p_at, src + codes);
+      cp16(stage + G::kCodes + p_key * (HD / 2) + p_at, src + codes);
     }
     if (s_lane >= 0 && s_block >= 0 && s_block < c.n_blocks) {
       const int key = tile * kTile + s_key, row = key - kv4_slot(c, key) * c.page_tokens;
-      cp16(stage + kTile * HD / 2 + G::kVStage + s_lane * 16,
+      cp16(stage + 2 * G::kCodes + s_lane * 16,
            kv4_page(c, s_block, head) + 2 * codes + ((s_lane >> 4) * c.page_tokens + row) * 4);
     }
     cp_commit();
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     __syncthreads();
     const uint32_t e8 = max(27u, __float_as_uint(fmaxf(red[r], red[kM + r])) >> 23);
     const float mul = __uint_as_float(e8 < 255u ? (267u - e8) << 23 : 0x3F800000u);
-    constexpr float kCode = P::kCentreK ? 1.f : 16777216.f;
+    constexpr float kCode = G::kValues || P::kCentreK ? 1.f : 16777216.f;
     k_mul = kCode / mul;
     z_mul = sum * mul * (1.f / kCode);
 #pragma unroll
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int n = 0; n < 4; ++n) {  // nibbles n and n + 4
-        const float m = n & 1 ? mul * 0.0625f : mul;
+        const float m = !G::kValues && (n & 1) ? mul * 0.0625f : mul;
         const float y0 = x[i][n] * m, y1 = x[i][4 + n] * m;
         hi[n] = pack_f16(y0, y1);
         const float2 back = unpack_f16(hi[n]);
@@ -233,10 +237,12 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
 
   float m = -INFINITY, off = 0.f;  // as for few rows; the same in both threads of a row
   F2 l2 = pair(0.f, 0.f), py2 = l2;
-  float o[HD / 2];  // dims hw * HD / 2 .. of the row
+  float o[HD / 2];  // of the row: columns hw HD / 2 .., dims hw HD / 4 .. and those HD / 2 further, in turn
 #pragma unroll
   for (int i = 0; i < HD / 2; ++i) o[i] = 0.f;
-  uint32_t v_exp = 41;
+  // biased exponents: V's largest scale (codes: P carries V's scales, times a
+  // power of two that makes it fit) or value, K's largest value
+  uint32_t v_exp = 41, k_exp = 41;
   bool ok = true;
   int n_done = 0;  // tiles before this one
   // adds the O of the tile before, which was computed meanwhile
@@ -268,56 +274,45 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     if (s_lane >= 0) s_block = page_of(tile + 2 * a.split, s_key);
 
     const uint8_t* stage = smem + G::kOps + buf * G::kStage;
-    // K: two words of a key (HD 64), four (HD 128), to units of its row
-    {
-      const int key = tid >> 2, part = tid & 3;
-#pragma unroll
-      for (int i = 0; i < G::kWords / 8; ++i) {
-        const uint2 w = *reinterpret_cast<const uint2*>(stage + key * (HD / 2) + i * 32 + part * 8);
-        uint8_t* row = smem + G::kK + buf * G::kKBytes + i * (kTile * 128) + key * 128;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t x = e ? w.y : w.x, y = x >> 8;
-          *reinterpret_cast<uint4*>(row + (((2 * part + e) ^ (key & 7)) << 4)) =
-              make_uint4(codes_even<P::kCentreK>(x), codes_odd<P::kCentreK>(x), codes_even<P::kCentreK>(y),
-                         codes_odd<P::kCentreK>(y));
-        }
-      }
-    }
-    // V: even or odd nibbles of half a word of eight keys, to two rows of V^T
-    {
-      const int kg = lane & 7, odd = warp & 1, half = (warp >> 1) & 1;
-#pragma unroll
-      for (int i = 0; i < G::kWords / 8; ++i) {
-        const int w = (lane >> 3) + 4 * (warp >> 2) + 8 * i;
-        const uint8_t* src = stage + kTile * HD / 2 + 8 * kg * (HD / 2) + kg * 16 + w * 4;
-        uint32_t x[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          x[n] = __byte_perm(*reinterpret_cast<const uint32_t*>(src + 2 * n * (HD / 2)),
-                             *reinterpret_cast<const uint32_t*>(src + (2 * n + 1) * (HD / 2)), half ? 0x7632 : 0x5410);
-        const int d = half * (HD / 2) + 4 * w + odd;
-        uint8_t* vt = smem + G::kV + buf * G::kVBytes;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t y[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t s = e ? x[n] >> 8 : x[n];
-            y[n] = odd ? codes_odd<P::kCentreV>(s) : codes_even<P::kCentreV>(s);
-          }
-          const int row = d + 2 * e;
-          *reinterpret_cast<uint4*>(vt + row * 128 + ((kg ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-      }
-    }
-    // the scales as floats, two keys a lane; zeros for keys without a place
-    float4* scales = reinterpret_cast<float4*>(smem + G::kScales);  // K's [32], V's [32]
-    if (warp == 0 || warp == 4) {
-      const uint32_t* sz = reinterpret_cast<const uint32_t*>(stage + kTile * HD / 2 + G::kVStage) + (hw ? kTile : 0);
+    const uint32_t* sz = reinterpret_cast<const uint32_t*>(stage + 2 * G::kCodes);  // K's [kTile], V's
+    float4* scales = reinterpret_cast<float4*>(smem + G::kScales);  // codes: K's [32], V's [32], two keys each
+    uint32_t v_new = v_exp;
+    int bad = INT_MAX;  // values: the first key whose V is NaN
+    __half2 vs2[2], vz2[2];  // values: scale and offset of this thread's key, of K and V
+    if constexpr (G::kValues) {
+      const uint2 kw = *reinterpret_cast<const uint2*>(sz + 2 * lane);
+      const uint2 vw = *reinterpret_cast<const uint2*>(sz + kTile + 2 * lane);
       const bool there = (have >> (lane >> 3)) & 1u;
-      const uint32_t wa = there && key0 + 2 * lane < n_keys ? sz[2 * lane] : 0u;
-      const uint32_t wb = there && key0 + 2 * lane + 1 < n_keys ? sz[2 * lane + 1] : 0u;
+      const bool ta = there && key0 + 2 * lane < n_keys, tb = there && key0 + 2 * lane + 1 < n_keys;
+      auto reach = [](uint32_t w) {  // the row's largest size; 0 if it is NaN
+        const float s = __uint_as_float(w << 16), z = __uint_as_float(w & 0xFFFF0000u);
+        return fmaxf(fmaxf(0.f, fabsf(z)), fabsf(fmaf(15.f, s, z)));
+      };
+      const float kt = fmaxf(ta ? reach(kw.x) : 0.f, tb ? reach(kw.y) : 0.f);
+      const float vt = fmaxf(ta ? reach(vw.x) : 0.f, tb ? reach(vw.y) : 0.f);
+      k_exp = max(k_exp, min(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(kt)) >> 23, 254u));
+      v_new = max(v_new, min(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vt)) >> 23, 254u));
+      const bool na = ta && (vw.x & 0x7FFF0000u) > 0x7F800000u, nb = tb && (vw.y & 0x7FFF0000u) > 0x7F800000u;
+      if (__any_sync(0xFFFFFFFFu, na || nb))
+        bad = (int)__reduce_min_sync(0xFFFFFFFFu, na ? 2 * lane : nb ? 2 * lane + 1 : INT_MAX);
+      // the thread's own key, values at 2^14..2^15 for the largest
+      const int key = tid >> 2;
+      const bool mine_there = ((have >> (key >> 4)) & 1u) && key0 + key < n_keys;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t w = mine_there ? sz[e * kTile + key] : 0u;
+        const float f = __uint_as_float((268u - (e ? v_new : k_exp)) << 23);
+        float z = __uint_as_float(w & 0xFFFF0000u);
+        if (e && z != z) z = 0.f;  // its NaN must not reach rows that do not see it
+        vs2[e] = __float2half2_rn(__uint_as_float(w << 16) * f);
+        vz2[e] = __float2half2_rn(z * f);
+      }
+    } else if (warp == 0 || warp == 4) {
+      // the scales as floats, two keys a lane; zeros for keys without a place
+      const uint32_t* half_sz = sz + (hw ? kTile : 0);
+      const bool there = (have >> (lane >> 3)) & 1u;
+      const uint32_t wa = there && key0 + 2 * lane < n_keys ? half_sz[2 * lane] : 0u;
+      const uint32_t wb = there && key0 + 2 * lane + 1 < n_keys ? half_sz[2 * lane + 1] : 0u;
       const bool centre = hw ? P::kCentreV : P::kCentreK;
       const float sa = __uint_as_float(wa << 16), sb = __uint_as_float(wb << 16);
       const float za = __uint_as_float(wa & 0xFFFF0000u), zb = __uint_as_float(wb & 0xFFFF0000u);
@@ -325,6 +320,44 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
           make_float4(sa, sb, centre ? fmaf(8.f, sa, za) : za, centre ? fmaf(8.f, sb, zb) : zb);
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(wa << 16, wb << 16));
       if (hw && lane == 0) s_vexp[buf] = min(top >> 23, 254u);
+    }
+    // K and V: words of a key to 16-byte units of its rows, two or four a thread
+    {
+      const int key = tid >> 2, part = tid & 3;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint8_t* rows_of = smem + (kv ? G::kV + buf * G::kVBytes : G::kK + buf * G::kKBytes) + key * 128;
+        auto even = [&](uint32_t x) -> uint32_t {
+          if constexpr (G::kValues) {
+            const uint32_t y = centred_even<0>(x);
+            const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), vs2[kv], vz2[kv]);
+            return *reinterpret_cast<const uint32_t*>(&v);
+          } else {
+            return kv ? codes_even<P::kCentreV>(x) : codes_even<P::kCentreK>(x);
+          }
+        };
+        const __half2 s16 = G::kValues ? __hmul2(vs2[kv], __float2half2_rn(0.0625f)) : __half2{};
+        auto odd = [&](uint32_t x) -> uint32_t {
+          if constexpr (G::kValues) {
+            const uint32_t y = centred_odd<0>(x);
+            const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), s16, vz2[kv]);
+            return *reinterpret_cast<const uint32_t*>(&v);
+          } else {
+            return kv ? codes_odd<P::kCentreV>(x) : codes_odd<P::kCentreK>(x);
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < G::kWords / 8; ++i) {
+          const uint2 w =
+              *reinterpret_cast<const uint2*>(stage + kv * G::kCodes + key * (HD / 2) + i * 32 + part * 8);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = e ? w.y : w.x, y = x >> 8;
+            *reinterpret_cast<uint4*>(rows_of + i * (kTile * 128) + (((2 * part + e) ^ (key & 7)) << 4)) =
+                make_uint4(even(x), odd(x), even(y), odd(y));
+          }
+        }
+      }
     }
     if (n_done && tid == 0) ok = ok && wait_products(&bars[1], (n_done - 1) & 1);  // S lies over the tile before's P
     fence_proxy_async_smem();  // the products read these generic-proxy writes
@@ -346,17 +379,20 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     ok = ok && wait_products(&bars[0], n_done & 1);
     tc_fence_after();
 
-    // the row's logits of 32 keys, in units of log2 times k_mul
+    // the row's logits of 32 keys, k_tile times them in units of log2
     float x[32];
     tmem_ld16x2(mine + G::kS + 32 * hw, x);
-    const F2 z2 = pair(z_mul, z_mul);
+    const float k_tile = G::kValues ? k_mul * __uint_as_float((k_exp - 14u) << 23) : k_mul;
     float top = -INFINITY;
+    if constexpr (!G::kValues) {
+      const F2 z2 = pair(z_mul, z_mul);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float4 ks = scales[16 * hw + i];
-      const float2 t = split(fma2(pair(ks.x, ks.y), pair(x[2 * i], x[2 * i + 1]), mul2(pair(ks.z, ks.w), z2)));
-      x[2 * i] = t.x;
-      x[2 * i + 1] = t.y;
+      for (int i = 0; i < 16; ++i) {
+        const float4 ks = scales[16 * hw + i];
+        const float2 t = split(fma2(pair(ks.x, ks.y), pair(x[2 * i], x[2 * i + 1]), mul2(pair(ks.z, ks.w), z2)));
+        x[2 * i] = t.x;
+        x[2 * i + 1] = t.y;
+      }
     }
     const bool part = have != 15u || key0 + kTile > all_see;
     if (part) {  // scores without a place, or behind the row's last key
@@ -370,35 +406,44 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     tc_fence_before();
     __syncthreads();  // and every S is read: P may lie over it
     tc_fence_after();
-    const float m_new = fmaxf(m, fmaxf(top, red[(hw ^ 1) * kM + r]) * k_mul);
-    const uint32_t e_new = max(v_exp, s_vexp[buf]);
-    if (m_new != m || e_new != v_exp) {
-      const float off_new = (m_new == -INFINITY ? 0.f : m_new) - (float)(141 - (int)e_new);
+    const float m_new = fmaxf(m, fmaxf(top, red[(hw ^ 1) * kM + r]) * k_tile);
+    if constexpr (!G::kValues) v_new = max(v_exp, s_vexp[buf]);
+    if (m_new != m || v_new != v_exp) {
+      // P reaches 2^15: as a weight, or times V's largest scale
+      const float off_new = (m_new == -INFINITY ? 0.f : m_new) - (G::kValues ? 15.f : (float)(141 - (int)v_new));
       const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
-      const F2 f2 = pair(fade, fade);
+      // operands that are values shrink as the largest one grows
+      const float o_fade = G::kValues ? fade * __uint_as_float(max(127 - (int)(v_new - v_exp), 0) << 23) : fade;
+      const F2 f2 = pair(fade, fade), o2 = pair(o_fade, o_fade);
       l2 = mul2(l2, f2);  // a NaN stays
-      py2 = mul2(py2, f2);
+      if (!G::kValues) py2 = mul2(py2, f2);
 #pragma unroll
       for (int i = 0; i < HD / 2; i += 2) {
-        const float2 t = split(mul2(pair(o[i], o[i + 1]), f2));
+        const float2 t = split(mul2(pair(o[i], o[i + 1]), o2));
         o[i] = t.x;
         o[i + 1] = t.y;
       }
       m = m_new;
       off = off_new;
-      v_exp = e_new;
+      v_exp = v_new;
     }
-    const F2 down = pair(-off, -off), k2 = pair(k_mul, k_mul);
+    if (bad <= last - key0) l2 = pair(NAN, NAN);  // `last` is -1 for rows without a key
+    const F2 down = pair(-off, -off), k2 = pair(k_tile, k_tile);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {  // 16 keys: 8 columns of P
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int n = 8 * g + i;
-        const float4 vs = scales[32 + 16 * hw + n];
         const float2 d = split(fma2(pair(x[2 * n], x[2 * n + 1]), k2, down));
-        const F2 p = pair(ex2(d.x), ex2(d.y));
+        const float2 pf = make_float2(ex2(d.x), ex2(d.y));
+        const F2 p = pair(pf.x, pf.y);
         l2 = add2(l2, p);
+        if constexpr (G::kValues) {
+          hi[i] = pack_f16(pf.x, pf.y);
+          continue;
+        }
+        const float4 vs = scales[32 + 16 * hw + n];
         // a key that the row does not see must not count, even with an offset of NaN
         const F2 y = part ? pair(x[2 * n] == -INFINITY ? 0.f : vs.z, x[2 * n + 1] == -INFINITY ? 0.f : vs.w)
                           : pair(vs.z, vs.w);
@@ -418,10 +463,12 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
-      constexpr uint32_t idesc = idesc_f16(kM, HD, false);
+      constexpr uint32_t idesc = idesc_f16(kM, HD, false) | 1u << 16;  // V is MN-major
 #pragma unroll
       for (int kk = 0; kk < kTile / 16; ++kk) {
-        const uint64_t vd = sdesc_k_sw128(smem0 + G::kV + buf * G::kVBytes + kk * 32);
+        // 16 keys: two groups of 8 rows; the next 64 dims are a leading offset away
+        const uint64_t vd = sdesc_k_sw128(smem0 + G::kV + buf * G::kVBytes + kk * 2048) +
+                            ((uint64_t)(kTile * 128 / 16 - 1) << 16);
         umma_f16_ta(tmem + G::kO, tmem + G::kS + 8 * kk, vd, idesc, kk > 0);
         if (P::kPLow) umma_f16_ta(tmem + G::kO, tmem + G::kS + 32 + 8 * kk, vd, idesc, 1u);
       }
@@ -443,36 +490,38 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     __syncthreads();
     const float py = red[r] + red[kM + r];
     __syncthreads();
-    // odd dims stand 16 times as high; raw codes at 2^-24
+    // codes: odd nibbles stand 16 times as high, raw ones at 2^-24; values at
+    // 2^14 / 2^v_exp, their weights at 2^15
     constexpr float even = P::kCentreV ? 1.f : 16777216.f;
+    const float back = __uint_as_float(v_exp - 29u << 23);
 #pragma unroll
-    for (int i = 0; i < HD / 2; i += 2) {
-      o[i] = fmaf(o[i], even, py);
-      o[i + 1] = fmaf(o[i + 1], even * 0.0625f, py);
-    }
+    for (int i = 0; i < HD / 2; ++i)
+      o[i] = G::kValues ? o[i] * back : fmaf(o[i], i >> 1 & 1 ? even * 0.0625f : even, py);
+    const float sum = G::kValues ? l * 0x1p-15f : l;
     const float none = ok ? 0.f : NAN;
     float* join = reinterpret_cast<float*>(smem);  // [kM][HD + 2]
     if (a.split == 1) {
       if (my_row < rows) {
         // a row that saw no key, or has no rotation, answers zeros
-        const float inv = l == 0.f || !placed ? 0.f : 1.0f / l;
-        T* dst = out + (int64_t)(q0 + my_new) * a.o_tok + my_head * a.o_head + hw * (HD / 2);
+        const float inv = sum == 0.f || !placed ? 0.f : 1.0f / sum;
+        T* dst = out + (int64_t)(q0 + my_new) * a.o_tok + my_head * a.o_head;
 #pragma unroll
-        for (int i = 0; i < HD / 2; i += 4) {
-          float y[4];
+        for (int i = 0; i < HD / 2; i += 8) {
+          float y[2][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = (inv == 0.f ? 0.f : o[i + e] * inv) + none;
-          store4(dst + i, y);
+          for (int e = 0; e < 8; ++e) y[e & 1][e >> 1] = (inv == 0.f ? 0.f : o[i + e] * inv) + none;
+          store4(dst + hw * (HD / 4) + i / 2, y[0]);
+          store4(dst + HD / 2 + hw * (HD / 4) + i / 2, y[1]);
         }
       }
       return;
     }
 #pragma unroll
-    for (int i = 0; i < HD / 2; i += 2)
-      *reinterpret_cast<float2*>(join + r * (HD + 2) + hw * (HD / 2) + i) = make_float2(o[i] + none, o[i + 1] + none);
+    for (int i = 0; i < HD / 2; ++i)
+      join[r * (HD + 2) + (i & 1) * (HD / 2) + hw * (HD / 4) + (i >> 1)] = o[i] + none;
     if (hw == 0) {
-      join[r * (HD + 2) + HD] = m == -INFINITY ? -INFINITY : off;
-      join[r * (HD + 2) + HD + 1] = l;
+      join[r * (HD + 2) + HD] = m == -INFINITY ? -INFINITY : G::kValues ? m : off;
+      join[r * (HD + 2) + HD + 1] = sum;
     }
     cluster_barrier();
     // each CTA joins every split-th row, 4 dims a thread
