@@ -39,6 +39,7 @@ constexpr int kM = 128;        // query rows of a CTA
 constexpr int kTile = 64;      // keys of a tile
 constexpr int kThreadsP = 256;
 constexpr int kSplits = 8;
+constexpr int kRing = 4;       // tiles in staging
 
 template <typename T, int HD>
 struct PGeo {
@@ -46,19 +47,27 @@ struct PGeo {
   static constexpr int kWords = HD / 8;                       // of a row's codes
   static constexpr int kQBytes = kM * HD * 2;                 // one of Q's parts
   static constexpr int kKBytes = kTile * HD * 2, kVBytes = HD * kTile * 2;
+  // operands, 1024-byte aligned: K twice and V three times, since a tile is
+  // expanded while the one before is multiplied
   static constexpr int kQ = 0, kQl = kQ + kQBytes, kK = kQl + (P::kQLow ? kQBytes : 0), kV = kK + 2 * kKBytes;
-  static constexpr int kOps = kV + 2 * kVBytes;               // operands: 1024-byte aligned
-  static constexpr int kCodes = kTile * HD / 2;               // staging: K's codes, V's, the scales
+  static constexpr int kOps = kV + 3 * kVBytes;
+  static constexpr int kCodes = kTile * HD / 2;               // staging: K's codes, V's, their scales
   static constexpr int kStage = 2 * kCodes + kTile * 8;
-  static constexpr int kScales = kOps + 2 * kStage;           // the tile's scales as floats
-  static constexpr int kRed = kScales + kTile * 16;           // [2][kM] floats: both threads of a row
+  static constexpr int kScales = kOps + kRing * kStage;       // what a tile's scales become, 1 KB each
+  static constexpr int kRed = kScales + kRing * kTile * 16;   // [2][kM] floats: both threads of a row
   static constexpr int kBytes = kRed + 2 * kM * 4;
   // after the keys: O [kM][HD], offsets, sums
   static constexpr int kJoin = kM * (HD + 2) * 4;
   static constexpr int kSmem = (kBytes > kJoin ? kBytes : kJoin) + 1024;  // and what aligns it
-  static constexpr int kS = 0, kO = 64, kCols = HD == 64 ? 128 : 256;  // TMEM: S (P over it), O
+  static constexpr int kS = 0, kP = 64, kO = 128, kCols = 256;  // TMEM: S, P (32 columns, 32 of what it lost), O
   static constexpr int kPerSm = HD == 64 ? 2 : 1;
   static constexpr bool kValues = P::kBf16;                   // operands hold values, not codes
+};
+
+struct Tile {  // what its scales say
+  uint32_t have;           // runs of 16 keys that have a place
+  uint32_t k_exp, v_exp;   // biased exponents so far: V's largest scale (codes) or value, K's largest value
+  int bad;                 // values: the first key whose V is NaN
 };
 
 struct PrefillArgs {
@@ -68,16 +77,28 @@ struct PrefillArgs {
   float scale_log2;
 };
 
-// Waits for a phase of the products' barrier; false after a second (nothing but
-// a lost product would take so long): the rows then answer NaN.
-__device__ __forceinline__ bool wait_products(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
+// Waits for a phase of a barrier; false after so many tries (more than a second,
+// and nothing but a lost copy or product would take so long): the rows then
+// answer NaN.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+  for (uint32_t it = 0; it < 1u << 26; ++it)
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 0 && globaltimer() - t0 > 1000000000ull) return false;
-  }
+  return false;
 }
+
+// 32 columns of a thread's TMEM lane at two addresses each, waited for together.
+__device__ __forceinline__ void tmem_ld32_two(uint32_t at_a, float* a, uint32_t at_b, float* b) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(a[8]), "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]), "=f"(a[16]), "=f"(a[17]), "=f"(a[18]), "=f"(a[19]), "=f"(a[20]), "=f"(a[21]), "=f"(a[22]), "=f"(a[23]), "=f"(a[24]), "=f"(a[25]), "=f"(a[26]), "=f"(a[27]), "=f"(a[28]), "=f"(a[29]), "=f"(a[30]), "=f"(a[31]),
+        "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15]), "=f"(b[16]), "=f"(b[17]), "=f"(b[18]), "=f"(b[19]), "=f"(b[20]), "=f"(b[21]), "=f"(b[22]), "=f"(b[23]), "=f"(b[24]), "=f"(b[25]), "=f"(b[26]), "=f"(b[27]), "=f"(b[28]), "=f"(b[29]), "=f"(b[30]), "=f"(b[31])
+      : "r"(at_a), "r"(at_b)
+      : "memory");
+}
+
+__device__ __forceinline__ void bar_pair(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
@@ -85,8 +106,9 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   using G = PGeo<T, HD>;
   using P = Keep<T>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2];  // S ready, O ready
-  __shared__ uint32_t s_tmem, s_vexp[2];
+  __shared__ __align__(8) uint64_t bars[2 + kRing];  // S ready, O ready, codes of a tile here
+  __shared__ Tile tiles[2 * kRing];  // a tile is copied before the one four earlier is done with
+  __shared__ uint32_t s_tmem;
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hw = warp >> 2;                    // half of the keys (S columns), and of the dims (O columns)
@@ -114,10 +136,10 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   const int n_keys = pos0 < 0 ? 0 : (int)min(hi_pos + 1, cap);
   const int all_see = (int)min(lo_pos + 1, cap);  // keys below it are seen by every row that has a position
   const int n_tiles = (n_keys + kTile - 1) / kTile;
+  const int n_mine = n_tiles > rank ? (n_tiles - rank + a.split - 1) / a.split : 0;  // every split-th tile
 
   if (tid == 0) {
-    mbar_init(&bars[0], 1);
-    mbar_init(&bars[1], 1);
+    for (int i = 0; i < 2 + kRing; ++i) mbar_init(&bars[i], i < 2 ? 1 : 4);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -125,44 +147,90 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     tmem_relinquish();
   }
 
-  // Copies of a tile: a thread takes one 16-byte piece of K's codes and one of
-  // V's (heads of 64: half of the threads), the last warp the scales as well.
-  constexpr int kPieces = kTile * HD / 2 / 16;  // of K, and of V: 128 or 256
+  // Each warp has a task of its own besides: warps 0 and 1 issue S and O, 2 and 3
+  // prepare K's and V's scales, 4 to 7 copy K's codes, V's, K's scales and V's.  A
+  // copy takes the runs of 16 keys that lie in one page: lane 0 (to 3, with pages
+  // that end in the tile) starts it.
   const int32_t* table = c.table + (int64_t)b * c.max_blocks;
-  const int codes = c.page_tokens * (HD / 2);
-  const int p_key = tid / (HD / 32), p_at = tid % (HD / 32) * 16;  // the piece's key in the tile, byte in its row
-  const int s_lane = tid - (kThreadsP - 32);                       // the last warp copies the scales, 4 keys a lane
-  const int s_key = 4 * (s_lane & 15);
-  auto page_of = [&](int tile, int key_in) -> int {
-    const int64_t key = (int64_t)tile * kTile + key_in;
-    return key < n_keys ? table[kv4_slot(c, (int)key)] : -1;
+  const int codes = c.page_tokens * (HD / 2), kind = warp & 3;
+  const int unit = kind < 2 ? HD / 2 : 4;  // bytes of a key
+  int block = -1;                          // of the next copy's run, looked up a tile ahead
+  auto look_up = [&](int j) {
+    const int64_t key = (int64_t)(rank + (int64_t)j * a.split) * kTile + 16 * (lane & 3);
+    block = j < n_mine && key < n_keys ? table[kv4_slot(c, (int)key)] : -1;
   };
-  auto copy = [&](int tile, int block, int s_block, uint8_t* stage) {
-    if (tid < kPieces && block >= 0 && block < c.n_blocks) {
-      const int key = tile * kTile + p_key, row = key - kv4_slot(c, key) * c.page_tokens;
-      const uint8_t* src = kv4_page(c, block, head) + row * (HD / 2) + p_at;
-      cp16(stage + p_key * (HD / 2) + p_at, src);
-      cp16(stage + G::kCodes + p_key * (HD / 2) + p_at, src + codes);
+  auto copy = [&](int j) {  // the CTA's j-th tile
+    if (j >= n_mine) return;
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, block >= 0 && block < c.n_blocks) & 15u;
+    uint64_t* bar = &bars[2 + (j & (kRing - 1))];
+    if (lane == 0) {
+      if (kind == 0) tiles[j & (2 * kRing - 1)].have = have;
+      mbar_arrive_expect_tx(bar, __popc(have) * 16 * unit);
     }
-    if (s_lane >= 0 && s_block >= 0 && s_block < c.n_blocks) {
-      const int key = tile * kTile + s_key, row = key - kv4_slot(c, key) * c.page_tokens;
-      cp16(stage + 2 * G::kCodes + s_lane * 16,
-           kv4_page(c, s_block, head) + 2 * codes + ((s_lane >> 4) * c.page_tokens + row) * 4);
+    __syncwarp();
+    if (lane < 4 && (have >> lane & 1u)) {
+      const int key = (rank + j * a.split) * kTile + 16 * lane, row = key - kv4_slot(c, key) * c.page_tokens;
+      if (lane == 0 || row == 0) {  // the run's page starts here
+        const int runs = min(min(4 - lane, (c.page_tokens - row) >> 4), (n_keys - key + 15) >> 4);
+        bulk_g2s(smem + G::kOps + (j & (kRing - 1)) * G::kStage + (kind >> 1) * (2 * G::kCodes) +
+                     ((kind & 1) * kTile + 16 * lane) * unit,
+                 kv4_page(c, block, head) + (kind >> 1) * (2 * codes) + ((kind & 1) * c.page_tokens + row) * unit,
+                 runs * 16 * unit, bar);
+      }
     }
-    cp_commit();
+    look_up(j + 1);
   };
-  int block = tid < kPieces ? page_of(rank, p_key) : -1, s_block = s_lane >= 0 ? page_of(rank, s_key) : -1;
-  // Runs of 16 keys that have a place, of the tile to come: each warp's first
-  // lanes look them up for themselves.
-  auto runs_of = [&](int tile) -> uint32_t {
-    int id = -1;
-    if (lane < 4) id = page_of(tile, 16 * lane);
-    return __ballot_sync(0xFFFFFFFFu, id >= 0 && id < c.n_blocks) & 15u;
+  bool ok = true;
+  auto arrived = [&](int j) { ok = ok && wait_bounded(&bars[2 + (j & (kRing - 1))], (j / kRing) & 1); };
+
+  // What the operands and the softmax need of a tile's scales, two keys a lane, of
+  // K (e = 0) or V; zeros for keys without a place.
+  uint32_t run_exp = 41;
+  auto prepare = [&](int j, int e) {
+    if (j >= n_mine) return;
+    arrived(j);
+    const int slot = j & (kRing - 1), key0 = (rank + j * a.split) * kTile;
+    Tile& tile = tiles[j & (2 * kRing - 1)];
+    uint2 w = *reinterpret_cast<const uint2*>(smem + G::kOps + slot * G::kStage + 2 * G::kCodes + e * (4 * kTile) +
+                                              8 * lane);
+    const bool there = (tile.have >> (lane >> 3)) & 1u;
+    if (!there || key0 + 2 * lane >= n_keys) w.x = 0;
+    if (!there || key0 + 2 * lane + 1 >= n_keys) w.y = 0;
+    const float sa = __uint_as_float(w.x << 16), sb = __uint_as_float(w.y << 16);
+    float za = __uint_as_float(w.x & 0xFFFF0000u), zb = __uint_as_float(w.y & 0xFFFF0000u);
+    if constexpr (G::kValues) {
+      // the largest size of the values, a NaN left out
+      const float ra = fmaxf(fmaxf(0.f, fabsf(za)), fabsf(fmaf(15.f, sa, za)));
+      const float rb = fmaxf(fmaxf(0.f, fabsf(zb)), fabsf(fmaf(15.f, sb, zb)));
+      run_exp = max(run_exp, min(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(ra, rb))) >> 23, 254u));
+      const float f = __uint_as_float((268u - run_exp) << 23);  // the largest value to 2^14..2^15
+      if (e) {  // a NaN must not reach rows that do not see it
+        const int bad = (int)__reduce_min_sync(0xFFFFFFFFu, za != za ? 2 * lane : zb != zb ? 2 * lane + 1 : INT_MAX);
+        if (lane == 0) tile.bad = bad;
+        if (za != za) za = 0.f;
+        if (zb != zb) zb = 0.f;
+      }
+      auto twice = [](float x) {
+        const __half2 h = __float2half2_rn(x);
+        return *reinterpret_cast<const uint32_t*>(&h);
+      };
+      reinterpret_cast<uint4*>(smem + G::kScales + slot * (kTile * 16))[32 * e + lane] =
+          make_uint4(twice(sa * f), twice(za * f), twice(sb * f), twice(zb * f));
+    } else {
+      const bool centre = e ? P::kCentreV : P::kCentreK;
+      reinterpret_cast<float4*>(smem + G::kScales + slot * (kTile * 16))[32 * e + lane] =
+          make_float4(sa, sb, centre ? fmaf(8.f, sa, za) : za, centre ? fmaf(8.f, sb, zb) : zb);
+      if (e) run_exp = max(run_exp, min(__reduce_max_sync(0xFFFFFFFFu, max(w.x << 16, w.y << 16)) >> 23, 254u));
+      if (lane == 0) tile.bad = INT_MAX;
+    }
+    if (lane == 0) (e ? tile.v_exp : tile.k_exp) = run_exp;
   };
-  copy(rank, block, s_block, smem + G::kOps);
-  uint32_t have_next = runs_of(rank);
-  if (tid < kPieces) block = page_of(rank + a.split, p_key);
-  if (s_lane >= 0) s_block = page_of(rank + a.split, s_key);
+
+  __syncthreads();  // the barriers are there for everyone
+  if (warp >= 4) {
+    look_up(0);
+    for (int j = 0; j < kRing; ++j) copy(j);
+  }
 
   // Q: the thread's half of the row's units, times scale log2(e) and the power of
   // two that brings the row's largest value to 2^13..2^14
@@ -232,6 +300,9 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (warp >> 1 == 1)
+    for (int j = 0; j < 3; ++j) prepare(j, warp & 1);
+  __syncthreads();
   const uint32_t tmem = s_tmem, mine = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t smem0 = smem_u32(smem);
 
@@ -240,149 +311,127 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   float o[HD / 2];  // of the row: columns hw HD / 2 .., dims hw HD / 4 .. and those HD / 2 further, in turn
 #pragma unroll
   for (int i = 0; i < HD / 2; ++i) o[i] = 0.f;
-  // biased exponents: V's largest scale (codes: P carries V's scales, times a
-  // power of two that makes it fit) or value, K's largest value
-  uint32_t v_exp = 41, k_exp = 41;
-  bool ok = true;
-  int n_done = 0;  // tiles before this one
-  // adds the O of the tile before, which was computed meanwhile
-  auto add_o = [&]() {
-    ok = ok && wait_products(&bars[1], (n_done - 1) & 1);
-    tc_fence_after();
+  uint32_t v_exp = 41;
+  auto add_part = [&](int i, const float* v) {  // 32 columns of a tile's O
 #pragma unroll
-    for (int i = 0; i < HD / 2; i += 32) {
-      float v[32];
-      tmem_ld16x2(mine + G::kO + hw * (HD / 2) + i, v);
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float2 t = split(add2(pair(o[i + e], o[i + e + 1]), pair(v[e], v[e + 1])));
-        o[i + e] = t.x;
-        o[i + e + 1] = t.y;
-      }
+    for (int e = 0; e < 32; e += 2) {
+      const float2 t = split(add2(pair(o[i + e], o[i + e + 1]), pair(v[e], v[e + 1])));
+      o[i + e] = t.x;
+      o[i + e + 1] = t.y;
     }
-    tc_fence_before();
   };
-#pragma unroll 1
-  for (int tile = rank; tile < n_tiles; tile += a.split, ++n_done) {
-    const int buf = n_done & 1, key0 = tile * kTile;
-    const uint32_t have = have_next;
-    cp_wait<0>();
-    __syncthreads();  // the tile's codes are here; every thread is done with the other staging buffer
-    copy(tile + a.split, block, s_block, smem + G::kOps + (buf ^ 1) * G::kStage);
-    have_next = runs_of(tile + a.split);
-    if (tid < kPieces) block = page_of(tile + 2 * a.split, p_key);
-    if (s_lane >= 0) s_block = page_of(tile + 2 * a.split, s_key);
-
-    const uint8_t* stage = smem + G::kOps + buf * G::kStage;
-    const uint32_t* sz = reinterpret_cast<const uint32_t*>(stage + 2 * G::kCodes);  // K's [kTile], V's
-    float4* scales = reinterpret_cast<float4*>(smem + G::kScales);  // codes: K's [32], V's [32], two keys each
-    uint32_t v_new = v_exp;
-    int bad = INT_MAX;  // values: the first key whose V is NaN
-    __half2 vs2[2], vz2[2];  // values: scale and offset of this thread's key, of K and V
-    if constexpr (G::kValues) {
-      const uint2 kw = *reinterpret_cast<const uint2*>(sz + 2 * lane);
-      const uint2 vw = *reinterpret_cast<const uint2*>(sz + kTile + 2 * lane);
-      const bool there = (have >> (lane >> 3)) & 1u;
-      const bool ta = there && key0 + 2 * lane < n_keys, tb = there && key0 + 2 * lane + 1 < n_keys;
-      auto reach = [](uint32_t w) {  // the row's largest size; 0 if it is NaN
-        const float s = __uint_as_float(w << 16), z = __uint_as_float(w & 0xFFFF0000u);
-        return fmaxf(fmaxf(0.f, fabsf(z)), fabsf(fmaf(15.f, s, z)));
-      };
-      const float kt = fmaxf(ta ? reach(kw.x) : 0.f, tb ? reach(kw.y) : 0.f);
-      const float vt = fmaxf(ta ? reach(vw.x) : 0.f, tb ? reach(vw.y) : 0.f);
-      k_exp = max(k_exp, min(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(kt)) >> 23, 254u));
-      v_new = max(v_new, min(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vt)) >> 23, 254u));
-      const bool na = ta && (vw.x & 0x7FFF0000u) > 0x7F800000u, nb = tb && (vw.y & 0x7FFF0000u) > 0x7F800000u;
-      if (__any_sync(0xFFFFFFFFu, na || nb))
-        bad = (int)__reduce_min_sync(0xFFFFFFFFu, na ? 2 * lane : nb ? 2 * lane + 1 : INT_MAX);
-      // the thread's own key, values at 2^14..2^15 for the largest
-      const int key = tid >> 2;
-      const bool mine_there = ((have >> (key >> 4)) & 1u) && key0 + key < n_keys;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t w = mine_there ? sz[e * kTile + key] : 0u;
-        const float f = __uint_as_float((268u - (e ? v_new : k_exp)) << 23);
-        float z = __uint_as_float(w & 0xFFFF0000u);
-        if (e && z != z) z = 0.f;  // its NaN must not reach rows that do not see it
-        vs2[e] = __float2half2_rn(__uint_as_float(w << 16) * f);
-        vz2[e] = __float2half2_rn(z * f);
-      }
-    } else if (warp == 0 || warp == 4) {
-      // the scales as floats, two keys a lane; zeros for keys without a place
-      const uint32_t* half_sz = sz + (hw ? kTile : 0);
-      const bool there = (have >> (lane >> 3)) & 1u;
-      const uint32_t wa = there && key0 + 2 * lane < n_keys ? half_sz[2 * lane] : 0u;
-      const uint32_t wb = there && key0 + 2 * lane + 1 < n_keys ? half_sz[2 * lane + 1] : 0u;
-      const bool centre = hw ? P::kCentreV : P::kCentreK;
-      const float sa = __uint_as_float(wa << 16), sb = __uint_as_float(wb << 16);
-      const float za = __uint_as_float(wa & 0xFFFF0000u), zb = __uint_as_float(wb & 0xFFFF0000u);
-      scales[32 * hw + lane] =
-          make_float4(sa, sb, centre ? fmaf(8.f, sa, za) : za, centre ? fmaf(8.f, sb, zb) : zb);
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(wa << 16, wb << 16));
-      if (hw && lane == 0) s_vexp[buf] = min(top >> 23, 254u);
+  // adds a tile's O but for its last 32 columns, whose address it gives
+  auto add_o = [&](int j) -> uint32_t {
+    ok = ok && wait_bounded(&bars[1], j & 1);
+    tc_fence_after();
+    if (HD == 128) {
+      float v[32];
+      tmem_ld16x2(mine + G::kO + hw * (HD / 2), v);
+      add_part(0, v);
     }
-    // K and V: words of a key to 16-byte units of its rows, two or four a thread
-    {
-      const int key = tid >> 2, part = tid & 3;
+    return mine + G::kO + hw * (HD / 2) + HD / 2 - 32;
+  };
+  // K's and V's words of a key to 16-byte units of its rows, two or four a thread
+  auto expand = [&](int j) {
+    arrived(j);
+    const int slot = j & (kRing - 1);
+    const uint8_t* stage = smem + G::kOps + slot * G::kStage;
+    const int key = tid >> 2, part = tid & 3;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint8_t* rows_of = smem + (kv ? G::kV + buf * G::kVBytes : G::kK + buf * G::kKBytes) + key * 128;
-        auto even = [&](uint32_t x) -> uint32_t {
-          if constexpr (G::kValues) {
-            const uint32_t y = centred_even<0>(x);
-            const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), vs2[kv], vz2[kv]);
-            return *reinterpret_cast<const uint32_t*>(&v);
-          } else {
-            return kv ? codes_even<P::kCentreV>(x) : codes_even<P::kCentreK>(x);
-          }
-        };
-        const __half2 s16 = G::kValues ? __hmul2(vs2[kv], __float2half2_rn(0.0625f)) : __half2{};
-        auto odd = [&](uint32_t x) -> uint32_t {
-          if constexpr (G::kValues) {
-            const uint32_t y = centred_odd<0>(x);
-            const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), s16, vz2[kv]);
-            return *reinterpret_cast<const uint32_t*>(&v);
-          } else {
-            return kv ? codes_odd<P::kCentreV>(x) : codes_odd<P::kCentreK>(x);
-          }
-        };
+    for (int kv = 0; kv < 2; ++kv) {
+      uint8_t* rows_of = smem + (kv ? G::kV + j % 3 * G::kVBytes : G::kK + (j & 1) * G::kKBytes) + key * 128;
+      __half2 s1{}, s16{}, z1{};
+      if constexpr (G::kValues) {
+        const uint2 w = reinterpret_cast<const uint2*>(smem + G::kScales + slot * (kTile * 16))[kTile * kv + key];
+        s1 = *reinterpret_cast<const __half2*>(&w.x);
+        z1 = *reinterpret_cast<const __half2*>(&w.y);
+        s16 = __hmul2(s1, __float2half2_rn(0.0625f));
+      }
+      auto even = [&](uint32_t x) -> uint32_t {
+        if constexpr (G::kValues) {
+          const uint32_t y = centred_even<0>(x);
+          const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), s1, z1);
+          return *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          return kv ? codes_even<P::kCentreV>(x) : codes_even<P::kCentreK>(x);
+        }
+      };
+      auto odd = [&](uint32_t x) -> uint32_t {
+        if constexpr (G::kValues) {
+          const uint32_t y = centred_odd<0>(x);
+          const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), s16, z1);
+          return *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          return kv ? codes_odd<P::kCentreV>(x) : codes_odd<P::kCentreK>(x);
+        }
+      };
 #pragma unroll
-        for (int i = 0; i < G::kWords / 8; ++i) {
-          const uint2 w =
-              *reinterpret_cast<const uint2*>(stage + kv * G::kCodes + key * (HD / 2) + i * 32 + part * 8);
+      for (int i = 0; i < G::kWords / 8; ++i) {
+        const uint2 w =
+            *reinterpret_cast<const uint2*>(stage + kv * G::kCodes + key * (HD / 2) + i * 32 + part * 8);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t x = e ? w.y : w.x, y = x >> 8;
-            *reinterpret_cast<uint4*>(rows_of + i * (kTile * 128) + (((2 * part + e) ^ (key & 7)) << 4)) =
-                make_uint4(even(x), odd(x), even(y), odd(y));
-          }
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = e ? w.y : w.x, y = x >> 8;
+          *reinterpret_cast<uint4*>(rows_of + i * (kTile * 128) + (((2 * part + e) ^ (key & 7)) << 4)) =
+              make_uint4(even(x), odd(x), even(y), odd(y));
         }
       }
     }
-    if (n_done && tid == 0) ok = ok && wait_products(&bars[1], (n_done - 1) & 1);  // S lies over the tile before's P
     fence_proxy_async_smem();  // the products read these generic-proxy writes
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      constexpr uint32_t idesc = idesc_f16(kM, kTile, false);
+  };
+  auto issue_s = [&](int j) {
+    constexpr uint32_t idesc = idesc_f16(kM, kTile, false);
 #pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk) {
-        const uint64_t kd = sdesc_k_sw128(smem0 + G::kK + buf * G::kKBytes + (kk >> 2) * (kTile * 128) + (kk & 3) * 32);
-        const uint32_t qa = (kk >> 2) * (kM * 128) + (kk & 3) * 32;
-        umma_f16(tmem + G::kS, sdesc_k_sw128(smem0 + G::kQ + qa), kd, idesc, kk > 0);
-        if (P::kQLow) umma_f16(tmem + G::kS, sdesc_k_sw128(smem0 + G::kQl + qa), kd, idesc, 1u);
-      }
-      umma_commit(&bars[0]);
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const uint64_t kd =
+          sdesc_k_sw128(smem0 + G::kK + (j & 1) * G::kKBytes + (kk >> 2) * (kTile * 128) + (kk & 3) * 32);
+      const uint32_t qa = (kk >> 2) * (kM * 128) + (kk & 3) * 32;
+      umma_f16(tmem + G::kS, sdesc_k_sw128(smem0 + G::kQ + qa), kd, idesc, kk > 0);
+      if (P::kQLow) umma_f16(tmem + G::kS, sdesc_k_sw128(smem0 + G::kQl + qa), kd, idesc, 1u);
     }
-    if (n_done) add_o();
-    ok = ok && wait_products(&bars[0], n_done & 1);
+    umma_commit(&bars[0]);
+  };
+  auto issue_o = [&](int j) {
+    constexpr uint32_t idesc = idesc_f16(kM, HD, false) | 1u << 16;  // V is MN-major
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk) {
+      // 16 keys: two groups of 8 rows; the next 64 dims are a leading offset away
+      const uint64_t vd = sdesc_k_sw128(smem0 + G::kV + j % 3 * G::kVBytes + kk * 2048) +
+                          ((uint64_t)(kTile * 128 / 16 - 1) << 16);
+      umma_f16_ta(tmem + G::kO, tmem + G::kP + 8 * kk, vd, idesc, kk > 0);
+      if (P::kPLow) umma_f16_ta(tmem + G::kO, tmem + G::kP + 32 + 8 * kk, vd, idesc, 1u);
+    }
+    umma_commit(&bars[1]);
+  };
+
+  if (n_mine) {
+    expand(0);
+    __syncthreads();
+    if (tid == 0) issue_s(0);
+    if (warp >= 4) copy(kRing);
+  }
+#pragma unroll 1
+  for (int j = 0; j < n_mine; ++j) {
+    // While S of this tile and O of the one before are computed, the next tile is
+    // expanded.
+    const int key0 = (rank + j * a.split) * kTile;
+    if (j + 1 < n_mine) expand(j + 1);
+    const uint32_t rest = j ? add_o(j - 1) : 0u;
+    const Tile tile = tiles[j & (2 * kRing - 1)];
+    const float4* scales = reinterpret_cast<const float4*>(smem + G::kScales + (j & (kRing - 1)) * (kTile * 16));
+    ok = ok && wait_bounded(&bars[0], j & 1);
     tc_fence_after();
 
     // the row's logits of 32 keys, k_tile times them in units of log2
     float x[32];
-    tmem_ld16x2(mine + G::kS + 32 * hw, x);
-    const float k_tile = G::kValues ? k_mul * __uint_as_float((k_exp - 14u) << 23) : k_mul;
+    if (j) {
+      float v[32];
+      tmem_ld32_two(mine + G::kS + 32 * hw, x, rest, v);
+      add_part(HD / 2 - 32, v);
+    } else {
+      tmem_ld16x2(mine + G::kS + 32 * hw, x);
+    }
+    const float k_tile = G::kValues ? k_mul * __uint_as_float((tile.k_exp - 14u) << 23) : k_mul;
     float top = -INFINITY;
     if constexpr (!G::kValues) {
       const F2 z2 = pair(z_mul, z_mul);
@@ -394,20 +443,18 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
         x[2 * i + 1] = t.y;
       }
     }
-    const bool part = have != 15u || key0 + kTile > all_see;
+    const bool part = tile.have != 15u || key0 + kTile > all_see;
     if (part) {  // scores without a place, or behind the row's last key
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (!((have >> (2 * hw + (i >> 4))) & 1u) || key0 + 32 * hw + i > last) x[i] = -INFINITY;
+        if (!((tile.have >> (2 * hw + (i >> 4))) & 1u) || key0 + 32 * hw + i > last) x[i] = -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
     red[hw * kM + r] = top;
-    tc_fence_before();
-    __syncthreads();  // and every S is read: P may lie over it
-    tc_fence_after();
+    bar_pair(1 + (warp & 3));  // the other half of the rows is the other warp's of the four
     const float m_new = fmaxf(m, fmaxf(top, red[(hw ^ 1) * kM + r]) * k_tile);
-    if constexpr (!G::kValues) v_new = max(v_exp, s_vexp[buf]);
+    const uint32_t v_new = tile.v_exp;
     if (m_new != m || v_new != v_exp) {
       // P reaches 2^15: as a weight, or times V's largest scale
       const float off_new = (m_new == -INFINITY ? 0.f : m_new) - (G::kValues ? 15.f : (float)(141 - (int)v_new));
@@ -427,7 +474,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       off = off_new;
       v_exp = v_new;
     }
-    if (bad <= last - key0) l2 = pair(NAN, NAN);  // `last` is -1 for rows without a key
+    if (tile.bad <= last - key0) l2 = pair(NAN, NAN);  // `last` is -1 for rows without a key
     const F2 down = pair(-off, -off), k2 = pair(k_tile, k_tile);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {  // 16 keys: 8 columns of P
@@ -455,28 +502,31 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
           lo[i] = pack_f16(w.x - back.x, w.y - back.y);
         }
       }
-      tmem_st8(mine + G::kS + 16 * hw + 8 * g, hi);
-      if (P::kPLow) tmem_st8(mine + G::kS + 32 + 16 * hw + 8 * g, lo);
+      tmem_st8(mine + G::kP + 16 * hw + 8 * g, hi);
+      if (P::kPLow) tmem_st8(mine + G::kP + 32 + 16 * hw + 8 * g, lo);
     }
     tmem_st_wait();
     tc_fence_before();
     __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      constexpr uint32_t idesc = idesc_f16(kM, HD, false) | 1u << 16;  // V is MN-major
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk) {
-        // 16 keys: two groups of 8 rows; the next 64 dims are a leading offset away
-        const uint64_t vd = sdesc_k_sw128(smem0 + G::kV + buf * G::kVBytes + kk * 2048) +
-                            ((uint64_t)(kTile * 128 / 16 - 1) << 16);
-        umma_f16_ta(tmem + G::kO, tmem + G::kS + 8 * kk, vd, idesc, kk > 0);
-        if (P::kPLow) umma_f16_ta(tmem + G::kO, tmem + G::kS + 32 + 8 * kk, vd, idesc, 1u);
-      }
-      umma_commit(&bars[1]);
+    tc_fence_after();
+    if (warp >= 4)
+      copy(j + 1 + kRing);  // where the tile was that is expanded now
+    else if (warp >= 2)
+      prepare(j + 3, warp & 1);
+    else if (lane == 0) {
+      if (warp == 1)
+        issue_o(j);
+      else if (j + 1 < n_mine)
+        issue_s(j + 1);
     }
+    __syncwarp();
   }
-  if (n_done) add_o();
-  cp_wait<0>();  // before this memory holds other things
+  if (n_mine) {
+    float v[32];
+    tmem_ld16x2(add_o(n_mine - 1), v);
+    add_part(HD / 2 - 32, v);
+    tc_fence_before();
+  }
   ok = __syncthreads_and(ok);
   if (warp == 0) tmem_dealloc(tmem, G::kCols);
   // a thread of each half holds its dims of the row; the sums come together
@@ -565,11 +615,15 @@ cudaError_t launch(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, Pref
     if (e != cudaSuccess) return e;
     if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  // CTAs that share a block's keys, while the GPU (148 SMs) is not full and each
-  // has some tiles
-  const int64_t tiles = ((int64_t)d.max_blocks * d.page_tokens + kTile - 1) / kTile;
+  // CTAs that share a block's keys: while the GPU (148 SMs) is not full, and once
+  // more between one wave and two, where sequences of other lengths leave the last
+  // wave half empty (512 blocks of 3000 keys on average: 233 us whole, 211 in two,
+  // 278 in four, since a CTA's start costs as much as 4 tiles)
+  const int64_t tiles = ((int64_t)d.max_blocks * d.page_tokens + kTile - 1) / kTile, wave = 148 * G::kPerSm;
   a.split = 1;
-  while (a.split < kSplits && items * a.split * 2 <= 148 * G::kPerSm && tiles >= a.split * 8) a.split *= 2;
+  while (a.split < kSplits && tiles >= a.split * 8 &&
+         (items * a.split * 2 <= wave || (items * a.split > wave && items * a.split < 2 * wave)))
+    a.split *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * a.split));
   cfg.blockDim = dim3(kThreadsP);
