@@ -187,7 +187,7 @@ def _check_attention(got, q64, kvs, past, counts, dtype, scale):
     """|error| <= half a step of the output's type, and of the arithmetic: each logit is a sum of hd
     products in fp32 (and of about 24 further roundings of 2^-24 of its terms' sizes), which changes
     a weight by e^d - 1 < 1.01 d; a weight is rounded to 2^-12 for bf16 (fp16 operand), to 2^-21 for
-    the others.  The weights multiply s c and z of a value v = s c + z, not v: sum p (s c + |z|), which
+    fp32 (fp16 is held to the same, though one of its weights alone may be off by 2^-12).  The weights multiply s c and z of a value v = s c + z, not v: sum p (s c + |z|), which
     R.attention gives as `bulk`, is what a relative error of the weights can move the sum by.  Both
     sums of the quotient carry this."""
     torch = _torch()
