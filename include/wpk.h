@@ -150,6 +150,16 @@ typedef struct wpk_plan_cfg {
   int head_workers;     /* frame_chunks >= 2: worker CTAs of the head programs
                            (0 = half of the workers); the backbones take the
                            rest of n_workers (0 = #SMs x workers_per_sm)        */
+  int kv_bits;          /* 0 or 16: bf16 pages.  4: 4-bit pages (the layout of
+                           wpk_kv4_cache, one run of [max_batch * max_blocks]
+                           pages per layer), which take 72 bytes per token and
+                           kv head where bf16 ones take 256.  A step's
+                           attention is then two launches per layer, the append
+                           of the step's K and V rows and the attention over the
+                           pages, so it needs WPK_PER_OP_GRAPH, CUDA-core decode,
+                           token-by-token prefill (the automatic choices then)
+                           and page_tokens % 16 == 0; no two-stage model, no
+                           wpk_prefill_slots                                    */
 } wpk_plan_cfg;
 
 /* Host weights: bf16 bit patterns, row-major [out][in]. */

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "graph.h"
+#include "kv4_host.h"
 
 namespace wpk {
 size_t worker_smem_bytes(int n_stages, int stage_bytes, int act_bytes);
@@ -65,6 +66,10 @@ struct wpk_handle {
   LayerDev* d_layers = nullptr;
   float2* d_rope = nullptr;
   int32_t* d_block_table = nullptr;
+  // 4-bit pages: the step's K and V rows [max_batch][n_kv][2][head_dim] (bf16)
+  // and the table that makes the QKV tiles write them there, [max_batch][max_context]
+  uint16_t* d_kv_rows = nullptr;
+  int32_t* d_kv_rows_table = nullptr;
   uint32_t* d_arrive = nullptr;
   uint32_t* d_rb_arrive = nullptr;  // batched decode: split arrivals per O / down row block
   ResDev* d_res = nullptr;          // resident grid: device copy of the doorbell
@@ -314,6 +319,12 @@ KParams make_params(const wpk_handle* h) {
   return P;
 }
 
+size_t kv4_layer_bytes(const wpk_handle* h) {  // one layer's 4-bit pages
+  int64_t page = 0;
+  wpk_kv4_page_bytes(h->g.m.head_dim, h->g.plan.page_tokens, &page);
+  return (size_t)h->n_blocks * h->g.m.n_kv_heads * (size_t)page;
+}
+
 void scratch_layout(wpk_handle* h) {
   const CompiledGraph& g = h->g;
   const wpk_model_cfg& m = g.m;
@@ -356,6 +367,7 @@ void scratch_layout(wpk_handle* h) {
   h->scratch_bytes = off;
   h->n_blocks = (int64_t)B * g.max_blocks;
   h->kv_bytes = (size_t)m.n_layers * h->n_blocks * 2 * m.n_kv_heads * g.plan.page_tokens * m.head_dim * 2;
+  if (g.plan.kv_bits == 4) h->kv_bytes = (size_t)m.n_layers * kv4_layer_bytes(h);
 }
 
 // A worker grid: cooperative, so that all its CTAs are co-resident, unless
@@ -380,6 +392,25 @@ int launch_megakernel(wpk_handle* h, const KParams& base, cudaStream_t s) {
   return WPK_OK;
 }
 
+// 4-bit pages, the attention of one layer: the rows that the QKV tiles have
+// left in d_kv_rows go to the layer's pages, then every sequence attends.
+int launch_kv4_attention(wpk_handle* h, int layer, const KParams& P, cudaStream_t s) {
+  const wpk_model_cfg& m = h->g.m;
+  const Plan& p = h->g.plan;
+  const wpk_kv4_cache cache{reinterpret_cast<uint8_t*>(h->kv) + (size_t)layer * kv4_layer_bytes(h), h->d_block_table,
+                            h->n_blocks, p.max_batch, h->g.max_blocks, m.n_kv_heads, m.head_dim, p.page_tokens};
+  Kv4Dev d;
+  int rc = kv4_view(&cache, h->d_seqlen, nullptr, p.max_batch, WPK_BF16, nullptr, 0, &d);
+  if (rc) return rc;
+  d.n_seq = h->d_active;
+  const int64_t hd = m.head_dim;
+  const Kv4Tensor k{h->d_kv_rows, 2 * hd * m.n_kv_heads, 2 * hd}, v{h->d_kv_rows + hd, k.token, k.head};
+  rc = kv4_append_launch(d, m.head_dim, k, v, WPK_BF16, nullptr, s);
+  if (rc) return rc;
+  const Kv4Tensor q{P.qbuf, P.q_rows, hd}, o{P.attn, P.q_rows, hd};
+  return kv4_attention_launch(d, m.head_dim, 1, q, m.n_heads, WPK_F32, nullptr, 0.f, o, s);
+}
+
 int capture_per_op(wpk_handle* h, int32_t* out_tok, float* logits, GraphEntry* out) {
   const CompiledGraph& g = h->g;
   if (!h->capture_stream) CUDA_TRY(h, cudaStreamCreateWithFlags(&h->capture_stream, cudaStreamNonBlocking));
@@ -387,12 +418,31 @@ int capture_per_op(wpk_handle* h, int32_t* out_tok, float* logits, GraphEntry* o
   base.in_tok = nullptr;
   base.out_tok = out_tok;
   base.logits = logits;
+  const bool kv4 = g.plan.kv_bits == 4;
+  if (kv4) {  // sequence b's row of either kind is "page" b, of one token, at any position
+    base.kv = h->d_kv_rows;
+    base.block_table = h->d_kv_rows_table;
+    base.max_blocks = g.plan.max_context;
+    base.page_tokens = 1;
+    base.n_blocks = 0;  // the same rows for every layer
+  }
   CUDA_TRY(h, cudaStreamBeginCapture(h->capture_stream, cudaStreamCaptureModeThreadLocal));
   for (const OpGroup& og : g.groups) {
     KParams P = base;
     P.t_begin = og.begin;
     P.t_end = og.end;
     P.per_op = 1;
+    if (kv4 && og.op == OP_ATTN) {
+      const int rc = launch_kv4_attention(h, og.layer, P, h->capture_stream);
+      if (rc) {
+        const std::string msg = g_build_error;
+        cudaGraph_t junk = nullptr;
+        cudaStreamEndCapture(h->capture_stream, &junk);
+        if (junk) cudaGraphDestroy(junk);
+        return fail(h, rc, "4-bit attention capture: " + msg);
+      }
+      continue;
+    }
     if (!P.dec_mma) {
       P.gemv_cps = gemv_chunks_per_stage(g.plan.per_op_slot);
       P.stage_bytes = P.gemv_cps * kStageBytes;
@@ -783,7 +833,9 @@ static int setup_device(wpk_handle* h) {
                o_sb = take((g.stream_begin.size() + 1) * 4), o_st = take((g.stream.size() + 1) * 4),
                o_pa = take((size_t)std::max(1, g.W) * 4),
                o_rb = take((size_t)model->n_layers * 2 * (model->hidden / 128 + 1) * 4),
-               o_res = take(sizeof(ResDev));
+               o_res = take(sizeof(ResDev)),
+               o_kvr = take(p.kv_bits == 4 ? B * model->n_kv_heads * 2 * model->head_dim * 2 : 0),
+               o_kvt = take(p.kv_bits == 4 ? B * p.max_context * 4 : 0);
   CUDA_TRY(h, cudaMalloc(&h->d_base, off));
   CUDA_TRY(h, cudaMemset(h->d_base, 0, off));
   h->d_tiles = reinterpret_cast<Tile*>(h->d_base + o_tiles);
@@ -812,6 +864,13 @@ static int setup_device(wpk_handle* h) {
   }
   h->d_rb_arrive = reinterpret_cast<uint32_t*>(h->d_base + o_rb);
   h->d_res = reinterpret_cast<ResDev*>(h->d_base + o_res);
+  if (p.kv_bits == 4) {
+    h->d_kv_rows = reinterpret_cast<uint16_t*>(h->d_base + o_kvr);
+    h->d_kv_rows_table = reinterpret_cast<int32_t*>(h->d_base + o_kvt);
+    std::vector<int32_t> own(B * p.max_context);
+    for (size_t i = 0; i < own.size(); ++i) own[i] = (int32_t)(i / p.max_context);
+    CUDA_TRY(h, cudaMemcpy(h->d_kv_rows_table, own.data(), own.size() * 4, cudaMemcpyHostToDevice));
+  }
   CUDA_TRY(h, cudaMemcpy(h->d_tiles, g.tiles.data(), n_tiles * sizeof(Tile), cudaMemcpyHostToDevice));
   if (!g.sig.empty()) CUDA_TRY(h, cudaMemcpy(h->d_sig, g.sig.data(), g.sig.size() * 4, cudaMemcpyHostToDevice));
   CUDA_TRY(h, cudaMemcpy(h->d_layers, g.lay.layers.data(), g.lay.layers.size() * sizeof(LayerDev),
@@ -901,6 +960,10 @@ int wpk_build_graph(const wpk_model_cfg* model, const wpk_plan_cfg* plan, wpk_ha
   if (plan->frame_chunks < 0 || plan->frame_chunks > 8 || plan->head_workers < 0) {
     g_build_error = "frame_chunks must be 0..8 and head_workers >= 0";
     return WPK_ERR_INVALID_ARG;
+  }
+  if (model->n_codebooks > 0 && plan->kv_bits == 4) {
+    g_build_error = "4-bit pages serve the single decoder only";
+    return WPK_ERR_UNSUPPORTED;
   }
   if (model->n_codebooks > 0) return build_two_stage(model, plan, out);
   if (plan->frame_chunks > 1 || plan->head_workers) {

@@ -56,6 +56,14 @@ std::string normalize_plan(const wpk_model_cfg& m, const wpk_plan_cfg& in, Plan*
   p->max_context = in.max_context;
   p->page_tokens = in.page_tokens ? in.page_tokens : 64;
   if (p->page_tokens % 8 || p->page_tokens > 256) return "page_tokens must be a multiple of 8, <= 256";
+  p->kv_bits = in.kv_bits ? in.kv_bits : 16;
+  if (p->kv_bits != 16 && p->kv_bits != 4) return "kv_bits must be 16 or 4";
+  const bool kv4 = p->kv_bits == 4;
+  if (kv4 && p->page_tokens % 16) return "4-bit pages hold a multiple of 16 tokens";
+  if (kv4 && (in.mode != WPK_PER_OP_GRAPH || in.decode == WPK_DECODE_MMA || in.prefill == WPK_PREFILL_MMA)) {
+    *code = WPK_ERR_UNSUPPORTED;
+    return "4-bit pages need WPK_PER_OP_GRAPH, CUDA-core decode and token-by-token prefill";
+  }
   p->workers_per_sm = in.workers_per_sm ? in.workers_per_sm : 1;
   p->n_workers = in.n_workers;
   if (p->n_workers < 0 || p->workers_per_sm < 0 || p->workers_per_sm > 4) return "bad worker count";
@@ -110,7 +118,7 @@ std::string normalize_plan(const wpk_model_cfg& m, const wpk_plan_cfg& in, Plan*
   // faster with fewer, larger splits (64 KB measured best at batch 16 and 48)
   p->tile_bytes = in.tile_bytes ? in.tile_bytes
                                 : ((in.decode == WPK_DECODE_MMA ||
-                                    (in.decode == WPK_DECODE_AUTO && in.max_batch > kAutoGemvBatch))
+                                    (in.decode == WPK_DECODE_AUTO && !kv4 && in.max_batch > kAutoGemvBatch))
                                        ? 65536
                                        : 32768);
   if (p->tile_bytes < 1024 || p->tile_bytes > 1 << 20) return "tile_bytes must be in [1K, 1M]";
@@ -125,8 +133,9 @@ std::string normalize_plan(const wpk_model_cfg& m, const wpk_plan_cfg& in, Plan*
     const bool mma_ok = (qr + 2 * kvr) % 128 == 0 && m.hidden % 128 == 0 && (2 * m.ffn) % 128 == 0 &&
                         m.hidden % 64 == 0 && qr % 128 == 0 && m.ffn % 64 == 0 && kvr % 128 == 0;
     if (in.decode == WPK_DECODE_AUTO)
-      p->decode_mode = (in.max_batch > kAutoGemvBatch && in.max_batch <= kMaxMmaBatch && mma_ok) ? WPK_DECODE_MMA
-                                                                                                : WPK_DECODE_GEMV;
+      p->decode_mode = (!kv4 && in.max_batch > kAutoGemvBatch && in.max_batch <= kMaxMmaBatch && mma_ok)
+                           ? WPK_DECODE_MMA
+                           : WPK_DECODE_GEMV;
     else if (in.decode == WPK_DECODE_MMA) {
       if (!mma_ok) { *code = WPK_ERR_UNSUPPORTED; return "shapes do not fit the tensor-core decode tiles"; }
       if (in.max_batch > kMaxMmaBatch) { *code = WPK_ERR_SHAPE; return "tensor-core decode takes at most 128 sequences"; }
@@ -155,7 +164,7 @@ std::string normalize_plan(const wpk_model_cfg& m, const wpk_plan_cfg& in, Plan*
       if (p->dec_stages < 2) { *code = WPK_ERR_UNSUPPORTED; return "no room for the tensor-core decode ring"; }
     }
     if (in.prefill == WPK_PREFILL_AUTO)
-      p->prefill_mode = mma_ok ? WPK_PREFILL_MMA : WPK_PREFILL_TOKENWISE;
+      p->prefill_mode = mma_ok && !kv4 ? WPK_PREFILL_MMA : WPK_PREFILL_TOKENWISE;
     else if (in.prefill == WPK_PREFILL_MMA) {
       if (!mma_ok) { *code = WPK_ERR_UNSUPPORTED; return "shapes do not fit the tensor-core prefill tiles"; }
       p->prefill_mode = WPK_PREFILL_MMA;

@@ -69,7 +69,8 @@ class wpk_plan_cfg(C.Structure):
                 ("n_regions", C.c_int), ("region_cut", C.c_int * 4), ("trace", C.c_int),
                 ("wait_timeout_ns", C.c_uint64), ("slot_bytes", C.c_int), ("tile_bytes", C.c_int),
                 ("split_pages", C.c_int), ("lookahead", C.c_int), ("schedule", C.c_int), ("prefill", C.c_int),
-                ("decode", C.c_int), ("frame_chunks", C.c_int), ("head_workers", C.c_int)]
+                ("decode", C.c_int), ("frame_chunks", C.c_int), ("head_workers", C.c_int),
+                ("kv_bits", C.c_int)]
 
 
 _P16 = C.POINTER(C.c_uint16)
@@ -199,11 +200,11 @@ def plan_cfg(max_batch: int, max_context: int, mode: int = WPK_MEGAKERNEL, n_reg
              page_tokens: int = 0, n_workers: int = 0, workers_per_sm: int = 0, resident: int = 0,
              slot_bytes: int = 0, tile_bytes: int = 0, split_pages: int = 0, lookahead: int = 0,
              schedule: int = 0, prefill: int = 0, decode: int = 0, frame_chunks: int = 0,
-             head_workers: int = 0) -> wpk_plan_cfg:
+             head_workers: int = 0, kv_bits: int = 0) -> wpk_plan_cfg:
     cut = (C.c_int * 4)(*list(region_cut) + [0] * (4 - len(region_cut)))
     return wpk_plan_cfg(max_batch, max_context, page_tokens, n_workers, workers_per_sm, mode, resident, n_regions,
                         cut, trace, wait_timeout_ns, slot_bytes, tile_bytes, split_pages, lookahead, schedule,
-                        prefill, decode, frame_chunks, head_workers)
+                        prefill, decode, frame_chunks, head_workers, kv_bits)
 
 
 # ----------------------------------------------------------- thin wrappers --
@@ -591,6 +592,25 @@ class Engine:
             logits = torch.empty((B,) + self._logit_shape, dtype=torch.float32, device=dev)
         wpk_step(self.h, itp, out_tok.data_ptr(), logits.data_ptr() if logits is not None else 0, self._stream())
         return out_tok, logits
+
+    def sample(self, logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, **kw):
+        """A token per row of a step's (or prefill's) logits, drawn with the given uniform numbers; a
+        two-stage model's logits give a code per codebook, from uniform numbers and settings of the
+        same leading shape.  Arguments as for sample()."""
+        lead = logits.shape[:-1]
+        flat = lambda x: None if x is None else x.reshape(-1)
+        out = sample(logits.reshape(-1, logits.shape[-1]), flat(uniform), flat(temperature), flat(top_k),
+                     flat(top_p), flat(min_p), **kw)
+        return tuple(x.reshape(lead) for x in out) if isinstance(out, tuple) else out.reshape(lead)
+
+    def step_sampled(self, uniform, in_tok=None, **sampling):
+        """One decode step whose tokens are drawn from its logits (see sample()): returns them and the
+        logits.  Without in_tok the step continues from the greedy token, so a drawn sequence passes
+        the tokens of the step before."""
+        if hasattr(self.shape, "backbone"):
+            raise WpkError(WPK_ERR_UNSUPPORTED, "a two-stage frame feeds its codes back inside the step")
+        _, logits = self.step(in_tok, want_logits=True)
+        return self.sample(logits, uniform, **sampling), logits
 
     def close(self):
         if self.h:

@@ -124,3 +124,24 @@ def test_messages_belong_to_the_thread():
     t.join()
     assert seen == [b""] and b"head_dim" in W.load_library().wpk_last_error(None)
     assert C.sizeof(W.wpk_kv4_cache) == 48
+
+
+def test_plans_over_4_bit_pages():
+    import synth
+
+    shape = synth.TINY
+    build = lambda **kw: W.wpk_build_graph(W.model_cfg(shape), W.plan_cfg(3, 100, n_workers=16, **kw))  # noqa: E731
+    for kw in (dict(), dict(mode=W.WPK_PER_OP_GRAPH, decode=W.WPK_DECODE_MMA),
+               dict(mode=W.WPK_PER_OP_GRAPH, prefill=W.WPK_PREFILL_MMA)):
+        _refused(UNSUPPORTED, lambda: build(kv_bits=4, **kw), "4-bit")
+    for kw in (dict(kv_bits=8), dict(kv_bits=-4), dict(kv_bits=4, page_tokens=8), dict(kv_bits=4, page_tokens=24)):
+        _refused(ARGS, lambda: build(mode=W.WPK_PER_OP_GRAPH, **kw))
+    two = synth.TINY_TWO_STAGE
+    _refused(UNSUPPORTED, lambda: W.wpk_build_graph(W.model_cfg(two), W.plan_cfg(
+        2, 16, n_workers=16, mode=W.WPK_PER_OP_GRAPH, kv_bits=4)), "4-bit")
+    h = build(mode=W.WPK_PER_OP_GRAPH, kv_bits=4, page_tokens=32)
+    assert W.wpk_workspace_size(h)[1] == shape.n_layers * 3 * 4 * shape.n_kv_heads * 32 * 72
+    W.wpk_destroy(h)
+    h = build(mode=W.WPK_PER_OP_GRAPH, kv_bits=16, page_tokens=32)
+    assert W.wpk_workspace_size(h)[1] == shape.n_layers * 3 * 4 * shape.n_kv_heads * 32 * 256
+    W.wpk_destroy(h)
