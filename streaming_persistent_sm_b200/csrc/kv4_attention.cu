@@ -44,7 +44,20 @@ namespace {
 constexpr int kRows = 8;    // query rows of a CTA (the N of the P V product)
 constexpr int kKeys = 64;   // keys of a warp's step
 constexpr int kMaxSplit = 16;
-constexpr int kManyRows = 48;  // of a (sequence, kv head): the tcgen05 kernel's from here on
+
+// The tcgen05 kernel's calls: from 64 query rows a (sequence, kv head) on, where
+// this kernel would have much to do (blocks of 8 rows times the keys that a table
+// names).  Measured (us, this kernel / that one, bf16, heads of 64, 8 kv heads):
+// 16 sequences of 4096 keys: 48 rows 65 / 71, 64 rows 73 / 72, 128 rows 140 / 75;
+// of 512 keys: 96 rows 27 / 22, 128 rows 34 / 23; one of 4096: 128 rows 16 / 27.
+// fp16 and fp32 meet at 64 to 80 rows, heads of 128 at 56 to 64.
+constexpr int kManyRows = 64;
+constexpr int64_t kManyWork = 1 << 20;
+bool many_rows(const Kv4Dev& d, int64_t rows) {
+  return rows >= kManyRows && (rows + 7) / 8 * d.n_kv * d.batch >=
+                                  kManyWork / ((int64_t)d.max_blocks * d.page_tokens);
+}
+
 
 // A CTA of WARPS warps: 4, of which an SM holds four (three at head_dim 128), or
 // 12, one to an SM, where 16 CTAs a cluster would not fill the GPU otherwise.
@@ -619,7 +632,7 @@ int kv4_attention_launch(const Kv4Dev& d, int head_dim, int max_new, const Kv4Te
   a.row_blocks = (int)row_blocks;
   cudaError_t e;
   const bool wide = head_dim == 128;
-  if ((int64_t)a.max_new * a.group >= kManyRows)
+  if (many_rows(d, (int64_t)a.max_new * a.group))
     e = kv4_prefill_launch(d, head_dim, a.max_new, q, a.group, dtype, rope, a.scale_log2, out, s);
   else if (dtype == WPK_F32)
     e = wide ? choose<float, 128>(d, q, out, a, items, s) : choose<float, 64>(d, q, out, a, items, s);

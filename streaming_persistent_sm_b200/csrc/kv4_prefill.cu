@@ -70,6 +70,24 @@ struct Tile {  // what its scales say
   int bad;                 // values: the first key whose V is NaN
 };
 
+// Four values as they are in memory (zeros where there are none).
+template <typename T>
+struct Raw4 {
+  uint2 r;
+  __device__ __forceinline__ void load(bool on, const T* p) {
+    r = on ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
+  }
+  __device__ __forceinline__ void to(float* f) const { load4(reinterpret_cast<const T*>(&r), f); }
+};
+template <>
+struct Raw4<float> {
+  float4 r;
+  __device__ __forceinline__ void load(bool on, const float* p) {
+    r = on ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void to(float* f) const { f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w; }
+};
+
 struct PrefillArgs {
   int64_t q_tok, q_head, o_tok, o_head;
   const float* rope;
@@ -178,7 +196,6 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
                  runs * 16 * unit, bar);
       }
     }
-    look_up(j + 1);
   };
   bool ok = true;
   auto arrived = [&](int j) { ok = ok && wait_bounded(&bars[2 + (j & (kRing - 1))], (j / kRing) & 1); };
@@ -226,10 +243,31 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     if (lane == 0) (e ? tile.v_exp : tile.k_exp) = run_exp;
   };
 
+  // The first tiles' places and Q's values are under way together.
+  int first[kRing] = {};
+  if (warp >= 4) {
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) {
+      look_up(j);
+      first[j] = block;
+    }
+  }
+  constexpr int kU = G::kWords / 2;  // units of Q's row that the thread takes
+  Raw4<T> raw[kU][2];
+  const T* q_row = q + (int64_t)(q0 + my_new) * a.q_tok + my_head * a.q_head + 4 * hw * kU;
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
+    raw[i][0].load(placed, q_row + 4 * i);
+    raw[i][1].load(placed, q_row + HD / 2 + 4 * i);
+  }
   __syncthreads();  // the barriers are there for everyone
   if (warp >= 4) {
-    look_up(0);
-    for (int j = 0; j < kRing; ++j) copy(j);
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) {
+      block = first[j];
+      copy(j);
+    }
+    look_up(kRing);
   }
 
   // Q: the thread's half of the row's units, times scale log2(e) and the power of
@@ -237,18 +275,14 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   float* red = reinterpret_cast<float*>(smem + G::kRed);
   float k_mul, z_mul;  // a logit is k_mul (s S + z z_mul)
   {
-    constexpr int kU = G::kWords / 2;  // units of the thread
-    float x[kU][8];                    // dims 4u .. 4u + 3, then HD / 2 + 4u ..
+    float x[kU][8];  // dims 4u .. 4u + 3, then HD / 2 + 4u ..
     float top = 0.f, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int u = hw * kU + i;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      raw[i][0].to(x[i]);
+      raw[i][1].to(x[i] + 4);
       if (placed) {
-        const T* p = q + (int64_t)(q0 + my_new) * a.q_tok + my_head * a.q_head + 4 * u;
-        load4(p, x[i]);
-        load4(p + HD / 2, x[i] + 4);
         if (a.rope) {
           const float* cs = a.rope + (my_pos * (HD / 2) + 4 * u) * 2;
           float t[8];
@@ -301,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   __syncthreads();
   tc_fence_after();
   if (warp >> 1 == 1)
-    for (int j = 0; j < 3; ++j) prepare(j, warp & 1);
+    for (int j = 0; j < 2; ++j) prepare(j, warp & 1);
   __syncthreads();
   const uint32_t tmem = s_tmem, mine = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t smem0 = smem_u32(smem);
@@ -408,7 +442,11 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     expand(0);
     __syncthreads();
     if (tid == 0) issue_s(0);
-    if (warp >= 4) copy(kRing);
+    if (warp >= 4) {
+      copy(kRing);
+      look_up(kRing + 1);
+    }
+    if (warp >> 1 == 1) prepare(2, warp & 1);
   }
 #pragma unroll 1
   for (int j = 0; j < n_mine; ++j) {
@@ -509,9 +547,10 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp >= 4)
+    if (warp >= 4) {
       copy(j + 1 + kRing);  // where the tile was that is expanded now
-    else if (warp >= 2)
+      look_up(j + 2 + kRing);
+    } else if (warp >= 2)
       prepare(j + 3, warp & 1);
     else if (lane == 0) {
       if (warp == 1)
@@ -618,7 +657,8 @@ cudaError_t launch(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, Pref
   // CTAs that share a block's keys: while the GPU (148 SMs) is not full, and once
   // more between one wave and two, where sequences of other lengths leave the last
   // wave half empty (512 blocks of 3000 keys on average: 233 us whole, 211 in two,
-  // 278 in four, since a CTA's start costs as much as 4 tiles)
+  // 278 in four, since a CTA's start costs as much as 4 tiles; 8 blocks of 4096 keys
+  // in 8 parts each 27 us, in 16 31 us)
   const int64_t tiles = ((int64_t)d.max_blocks * d.page_tokens + kTile - 1) / kTile, wave = 148 * G::kPerSm;
   a.split = 1;
   while (a.split < kSplits && tiles >= a.split * 8 &&

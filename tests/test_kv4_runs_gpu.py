@@ -9,6 +9,14 @@ from tests.test_kv4_gpu import DTYPES, _filled, _i32, _indptr, _positions, _rows
 pytestmark = pytest.mark.gpu
 
 
+def _wide(table, page):
+    """The table with room for 2^17 tokens a sequence, without pages there: the tcgen05 kernel takes calls
+    of many rows over many keys, and it counts the keys that a table could name."""
+    torch = _torch()
+    more = (1 << 17) // page - table.shape[1]
+    return torch.cat([table, torch.full((table.shape[0], more), -1, dtype=torch.int32, device="cuda")], 1)
+
+
 def _check(got, q64, kvs, past, counts, dtype, scale):
     """|error| <= half a step of the output's type, and of the arithmetic (`bulk` and `reach` are
     R.attention's: the weighted sizes of the values' parts, the largest logit's sum of sizes).
@@ -33,7 +41,7 @@ def _check(got, q64, kvs, past, counts, dtype, scale):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("hd,kv,group,page,past,counts,rope", [
-    (64, 1, 48, 64, [5], [1], False),                          # one token of many heads: 48 rows
+    (64, 1, 64, 64, [5], [1], False),                          # one token of many heads: 64 rows
     (64, 1, 3, 16, [0, 63, 64, 65], [16, 17, 43, 85], True),   # pages that end inside a tile; 129 rows and more
     (128, 2, 4, 48, [10, 0, 0, 200], [31, 0, 1, 33], True),    # a sequence without new tokens, one with one
     (64, 2, 7, 256, [255, 256], [20, 55], False),
@@ -46,9 +54,25 @@ def test_runs_match_float64(dtype, hd, kv, group, page, past, counts, rope):
     c, table, kvs = _filled(rng, lens, kv, hd, page, dtype)
     q, q64 = _rows(rng, sum(counts), kv * group, hd, dtype)
     rt = W.rope_table(max(lens), hd, 500000.0) if rope else None
-    got = c.attention(q, _i32(past), table, indptr=_indptr(counts), max_new=max(counts), rope=rt)
+    got = c.attention(q, _i32(past), _wide(table, page), indptr=_indptr(counts), max_new=max(counts), rope=rt)
     if rope:
         q64 = R.rotate(q64, _positions(past, counts), rt.cpu().numpy())
+    _check(got, q64, kvs, past, counts, dtype, hd ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+def test_runs_of_many_sequences_fill_the_gpu(dtype, hd):
+    """Enough of them that no keys are split; their lengths and runs all differ."""
+    rng = np.random.default_rng(36)
+    B, kv, page = 80, 4, 64
+    counts = rng.integers(0, 21, B)
+    counts[3] = 20
+    past = rng.integers(0, 120, B)
+    c, table, kvs = _filled(rng, list(past + counts), kv, hd, page, dtype)
+    more = _torch().full((B, 7 - table.shape[1]), 1 << 20, dtype=_torch().int32, device="cuda")
+    q, q64 = _rows(rng, int(counts.sum()), 4 * kv, hd, dtype)
+    got = c.attention(q, _i32(past), _torch().cat([table, more], 1), indptr=_indptr(counts), max_new=20)
     _check(got, q64, kvs, past, counts, dtype, hd ** -0.5)
 
 
@@ -67,7 +91,7 @@ def test_runs_with_values_and_queries_of_any_size(dtype):
     c = W.KV4Cache(5, 1, hd, 64)
     table = _i32([[3, 1, 0, 2, 4]])
     c.append(k.cuda(), v.cuda(), _i32([0]), table)
-    got = c.attention(q.cuda(), _i32([n - 60]), table)
+    got = c.attention(q.cuda(), _i32([n - 60]), _wide(table, 64))
     _check(got, q.double().numpy(), [(R.held(k.double().numpy()), R.held(v.double().numpy()))], [n - 60], [60],
            dtype, hd ** -0.5)
 
@@ -81,7 +105,7 @@ def test_runs_leave_out_pages_and_sequences_without_a_place(dtype):
     t[1, 3] = -1               # 16 keys of sequence 1 are gone
     t[2, :] = 1 << 30          # all of sequence 2's
     q, q64 = _rows(rng, 4 * new, 4, 64, dtype)
-    got = c.attention(q, _i32([170, 170, 170, -1]), t)  # sequence 3 is idle
+    got = c.attention(q, _i32([170, 170, 170, -1]), _wide(t, 16))  # sequence 3 is idle
     assert (got[2 * new:] == 0).all()
     k, v = kvs[1]
     there = np.r_[0:48, 64:200]
@@ -100,11 +124,11 @@ def test_runs_keep_a_row_that_is_not_finite_to_the_queries_that_see_it(dtype, wh
     table = _i32([[0, 2, 1]])
     c.append(k, v, _i32([0]), table)
     q, q64 = _rows(rng, n, 2, 64, dtype)
-    got = c.attention(q, _i32([0]), table)
+    got = c.attention(q, _i32([0]), _wide(table, 64))
     assert got[70:].isnan().all() and not got[:70].isnan().any()
     _check(got[:70], q64[:70], [(R.held(k64[:70]), R.held(v64[:70]))], [0], [70], dtype, 0.125)
     q[3, 1, 0] = float("inf")  # a query that is not finite keeps to itself
-    other = c.attention(q, _i32([0]), table)
+    other = c.attention(q, _i32([0]), _wide(table, 64))
     assert other[3, 1].isnan().all()
     assert _torch().equal(other[:3], got[:3]) and _torch().equal(other[4:70], got[4:70])
 
@@ -116,7 +140,7 @@ def test_runs_stop_where_the_rotations_and_the_rows_do():
     q, q64 = _rows(rng, 60, 2, 64, "float32")
     rt = W.rope_table(90, 64, 500000.0)
     out = torch.full((60, 2, 64), 7.0, device="cuda")
-    c.attention(q, _i32([40]), table, indptr=_i32([0, 57]), max_new=60, rope=rt, out=out)
+    c.attention(q, _i32([40]), _wide(table, 64), indptr=_i32([0, 57]), max_new=60, rope=rt, out=out)
     assert (out[57:] == 7.0).all()               # behind the last sequence: left as they were
     assert (out[50:57] == 0.0).all()             # positions without a rotation
     _check(out[:50], R.rotate(q64[:50], np.arange(40, 90), rt.cpu().numpy()), kvs, [40], [50], "float32", 0.125)
@@ -129,7 +153,7 @@ def test_runs_on_other_streams_captured_and_twice_at_once(dtype):
     past, counts = [300, 0, 65], [40, 33, 64]
     c, table, _ = _filled(rng, [p + n for p, n in zip(past, counts)], 2, 64, 64, dtype)
     q, _ = _rows(rng, sum(counts), 8, 64, dtype)
-    pos, ip = _i32(past), _indptr(counts)
+    pos, ip, table = _i32(past), _indptr(counts), _wide(table, 64)
     run = lambda out: c.attention(q, pos, table, indptr=ip, max_new=64, out=out)  # noqa: E731
     want = run(None)
     outs = [torch.zeros_like(q) for _ in range(4)]
