@@ -466,7 +466,7 @@ typedef struct wpk_kv4_cache {
 int wpk_kv4_page_bytes(int head_dim, int page_tokens, int64_t *bytes);
 
 /* Append rows: K rotated to its position (rope_dev) and V, quantised.  The
- * rotation is computed in 64 bits.  Rows without a place are dropped.  Two rows
+ * codes are those of a rotation in 64 bits.  Rows without a place are dropped.  Two rows
  * of one call must not share a place (tables that share pages may only share
  * pages that this call does not write). */
 int wpk_kv4_append(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32_t *indptr_dev, int total,
