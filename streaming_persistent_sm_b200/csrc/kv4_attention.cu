@@ -25,6 +25,11 @@
 // memory: one launch, no workspace, no atomics, so the result does not depend
 // on timing.  Each warp streams its pages through its own ring of shared-memory
 // stages with 16-byte asynchronous copies; nothing spins.
+//
+// Bound by the instructions around the products, some 640 a warp's step, and for
+// little work by latency.  Measured: 32 sequences of up to 8192 keys, 32 heads of 64
+// over 8 kv heads, bf16: 40 us (2.8 TB/s of cache); one of 131072, 64 heads of 128
+// over 8, fp16: 93 us (1.5 TB/s); one of 624: 7.7 us.
 #include <limits.h>
 #include <math.h>
 
@@ -362,7 +367,8 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     const uint32_t e_new = max(v_exp, min(s_top >> 23, 254u));
     const float m_new = fmaxf(m, top);
     if (__any_sync(0xFFFFFFFFu, m_new != m || e_new != v_exp)) {
-      const float off_new = (m_new == -INFINITY ? 0.f : m_new) - (float)(141 - (int)e_new);  // 14 + 127
+      // 14 + 127; rounded up, so that P does not pass its range however large the logits are
+      const float off_new = __fsub_ru(m_new == -INFINITY ? 0.f : m_new, (float)(141 - (int)e_new));
       const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
       l2 = mul2(l2, pair(fade, fade));  // a NaN stays
       py2 = mul2(py2, pair(fade, fade));

