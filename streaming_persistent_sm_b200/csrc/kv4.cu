@@ -405,7 +405,7 @@ int kv4_view(const wpk_kv4_cache* cache, const int32_t* pos, const int32_t* indp
   d->n_kv = cache->n_kv_heads;
   d->page_tokens = cache->page_tokens;
   d->page_bytes = (int)bytes;
-  d->page_magic = ((1ull << 39) + cache->page_tokens - 1) / cache->page_tokens;
+  d->page_magic = kv4_page_magic(cache->page_tokens);
   d->pos = pos;
   d->indptr = indptr;
   d->n_seq = nullptr;

@@ -3,6 +3,8 @@
 #pragma once
 #include <stdint.h>
 
+#include "kv4_slot.h"
+
 namespace wpk {
 
 struct Kv4Dev {
@@ -10,7 +12,7 @@ struct Kv4Dev {
   const int32_t* table;  // [batch][max_blocks]
   int64_t n_blocks;
   int batch, max_blocks, n_kv, page_tokens, page_bytes;
-  unsigned long long page_magic;  // 2^39 / page_tokens, rounded up
+  uint64_t page_magic;   // kv4_page_magic(page_tokens)
   const int32_t* pos;     // [batch] position of a sequence's first new token; < 0 = idle
   const int32_t* indptr;  // [batch + 1], or NULL: `each` tokens per sequence
   const int32_t* n_seq;   // sequences in use (device), or NULL: batch
@@ -20,11 +22,7 @@ struct Kv4Dev {
 
 __device__ __forceinline__ int kv4_sequences(const Kv4Dev& c) { return c.n_seq ? min(c.batch, *c.n_seq) : c.batch; }
 
-// position / page_tokens, for 0 <= position < 2^31 and page_tokens <= 256: the
-// rounding of the factor adds less than 2^-8 <= 1 / page_tokens.
-__device__ __forceinline__ int kv4_slot(const Kv4Dev& c, int position) {
-  return (int)(((unsigned long long)(uint32_t)position * c.page_magic) >> 39);
-}
+__device__ __forceinline__ int kv4_slot(const Kv4Dev& c, int position) { return kv4_slot_of(position, c.page_magic); }
 
 // First byte of (block, kv head)'s page.
 __device__ __forceinline__ uint8_t* kv4_page(const Kv4Dev& c, int block, int head) {

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
   const int64_t lo_pos = pos0 + r0 / a.group, hi_pos = pos0 + (min(r0 + kRows, rows) - 1) / a.group;
   const int n_keys = pos0 < 0 ? 0 : (int)min(hi_pos + 1, cap);
   const int all_see = (int)min(lo_pos + 1, cap);  // keys below it are seen by every row that has a position
-  const int n_steps = (n_keys + kKeys - 1) / kKeys;
+  const int n_steps = n_keys ? (n_keys - 1) / kKeys + 1 : 0;
   const int codes = c.page_tokens * G::kRowBytes;
 
   uint8_t* ring = smem + warp * G::kWarpBytes;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       x[2 * n] = xs.x;
       x[2 * n + 1] = xs.y;
     }
-    const bool part = have != 15u || key0 + kKeys > all_see;
+    const bool part = have != 15u || key0 > all_see - kKeys;
     if (part) {  // scores without a place, or behind the row's last key
 #pragma unroll
       for (int n = 0; n < 8; ++n)
