@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
   for (int s = 0; s < G::kStages - 1; ++s) held |= issue(ring + s * G::kStageBytes) << (4 * s);
 
   // Q: lane (g, t) holds dims 4 WPL t .. + 4 WPL of both halves of row g, times
-  // scale log2(e) and a power of two that brings the rows' largest value to
-  // 2^13..2^14; K's scales take it back
+  // scale log2(e) and a power of two that brings the row's largest value to
+  // 2^13..2^14, each row by its own; k_mul takes it back
   uint32_t qa[2 * WPL][4];
   float k_mul, logit_z;
   {
@@ -249,11 +249,14 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       sum += lo[i] + hi[i];
     }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    for (int o = 1; o < 4; o <<= 1) {
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    }
     logit_z = sum;
     // exponent fields: the power of two is 2^(140 - e), within fp32 (rows of no
     // finite value, or below 2^-100, as they are)
-    const uint32_t e = max(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)) >> 23, 27u);
+    const uint32_t e = max(__float_as_uint(top) >> 23, 27u);
     const float mul = __uint_as_float(e < 255u ? (267u - e) << 23 : 0x3F800000u);
     k_mul = (P::kCentreK ? 1.f : 16777216.f) / mul;
 #pragma unroll
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
         const float z = __uint_as_float(w & 0xFFFF0000u);
         return centre ? fmaf(8.f, __uint_as_float(w << 16), z) : z;
       };
-      scales[lane] = make_float4(s_of(ka) * k_mul, s_of(kb) * k_mul, z_of(ka, P::kCentreK), z_of(kb, P::kCentreK));
+      scales[lane] = make_float4(s_of(ka), s_of(kb), z_of(ka, P::kCentreK), z_of(kb, P::kCentreK));
       scales[32 + lane] = make_float4(s_of(va), s_of(vb), z_of(va, P::kCentreV), z_of(vb, P::kCentreV));
       s_top = __reduce_max_sync(0xFFFFFFFFu, max(va << 16, vb << 16));
     }
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
 
     // S, and the logits in units of log2
     float x[16];
-    const F2 z2 = pair(logit_z, logit_z);
+    const F2 z2 = pair(logit_z, logit_z), k2 = pair(k_mul, k_mul);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       const float4 ks = scales[4 * n + t];
       F2 dot = pair(s[0], s[1]);
       if (P::kQLow) dot = add2(dot, pair(s[2], s[3]));
-      const float2 xs = split(fma2(pair(ks.x, ks.y), dot, mul2(pair(ks.z, ks.w), z2)));
+      const float2 xs = split(fma2(pair(ks.x, ks.y), mul2(dot, k2), mul2(pair(ks.z, ks.w), z2)));
       x[2 * n] = xs.x;
       x[2 * n + 1] = xs.y;
     }
