@@ -275,15 +275,15 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
   }
 
   // Running sums of the online softmax, all of them 2^-off times the true ones:
-  // off = m - (14 - exponent of the largest V scale so far), so that P s, which
-  // the second product takes in fp16, stays below 2^15 whatever the scales (one
-  // below 2^-86 counts as 2^-86).
+  // off = m - (14 - exponent of V's largest scale so far, see v_key_exp), so that
+  // P s, which the second product takes in fp16, stays below 2^15 whatever the
+  // scales, and P y within fp32.
   float m = -INFINITY, off = 0.f;  // of row g
   F2 l2 = pair(0.f, 0.f), py2 = l2;  // l and the sum of p y, of this lane's keys only, in two halves
   float o[2 * WPL][4];               // rows 2t, 2t + 1: dims 4g + .. of both halves
 #pragma unroll
   for (int i = 0; i < 2 * WPL; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  uint32_t v_exp = 41;
+  uint32_t v_exp = kLeastExp;
   int cur = 0;
 #pragma unroll 1
   for (int step = first; step < n_steps; step += stride) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     // the step's scales as floats: lane 4 n + t's keys are 8 n + t and 8 n + 7 - t,
     // as S's columns have them; zeros for keys without a place (whatever the stage
     // held)
-    uint32_t s_top;
+    uint32_t e_top;
     {
       const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * kKeys * G::kRowBytes);
       const int ja = 8 * g + t, jb = 8 * g + 7 - t;
@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
         return centre ? fmaf(8.f, __uint_as_float(w << 16), z) : z;
       };
       scales[lane] = make_float4(s_of(ka), s_of(kb), z_of(ka, P::kCentreK), z_of(kb, P::kCentreK));
-      scales[32 + lane] = make_float4(s_of(va), s_of(vb), z_of(va, P::kCentreV), z_of(vb, P::kCentreV));
-      s_top = __reduce_max_sync(0xFFFFFFFFu, max(va << 16, vb << 16));
+      const float4 vs = make_float4(s_of(va), s_of(vb), z_of(va, P::kCentreV), z_of(vb, P::kCentreV));
+      scales[32 + lane] = vs;
+      e_top = __reduce_max_sync(0xFFFFFFFFu, max(v_key_exp(vs.x, vs.z), v_key_exp(vs.y, vs.w)));
     }
     __syncwarp();
 
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     top = fmaxf(top, x[15]);
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const uint32_t e_new = max(v_exp, min(s_top >> 23, 254u));
+    const uint32_t e_new = max(v_exp, e_top);
     const float m_new = fmaxf(m, top);
     if (__any_sync(0xFFFFFFFFu, m_new != m || e_new != v_exp)) {
       // 14 + 127; rounded up, so that P does not pass its range however large the logits are

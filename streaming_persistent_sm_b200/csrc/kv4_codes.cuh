@@ -56,6 +56,16 @@ __device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
   return kCentre ? centred_odd(w) : w & kOdd;
 }
 
+// Exponent fields of V's scales that the weights of a row follow: a weight stays
+// below 2^(141 - field), so that times a scale s it is below 2^15, what an fp16
+// operand holds, and times an offset y below 2^79, which 2^31 keys sum up within
+// fp32.  A field below kLeastExp would let the sum of 2^31 weights overflow.
+constexpr uint32_t kLeastExp = 45;
+__device__ __forceinline__ uint32_t v_key_exp(float s, float y) {
+  const uint32_t es = (__float_as_uint(s) >> 23) & 255u, ey = (__float_as_uint(y) >> 23) & 255u;
+  return max(max(min(es, 254u), ey == 255u ? 0u : ey - min(ey, 64u)), kLeastExp);  // a NaN says nothing
+}
+
 // What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's
 // codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
 // that the output's rounding is off, relative, of random values).  fp16: Q to 22

@@ -69,7 +69,7 @@ struct PGeo {
 
 struct Tile {  // what its scales say
   uint32_t have;           // runs of 16 keys that have a place
-  uint32_t k_exp, v_exp;   // biased exponents so far: V's largest scale (codes) or value, K's largest value
+  uint32_t k_exp, v_exp;   // biased exponents so far: V's largest scale (codes, see v_key_exp) or value, K's largest value
   int bad;                 // values: the first key whose V is NaN
 };
 
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
 
   // What the operands and the softmax need of a tile's scales, two keys a lane, of
   // K (e = 0) or V; zeros for keys without a place.
-  uint32_t run_exp = 41;
+  uint32_t run_exp = kLeastExp;
   auto prepare = [&](int j, int e) {
     if (j >= n_mine) return;
     arrived(j);
@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
           make_uint4(twice(sa * f), twice(za * f), twice(sb * f), twice(zb * f));
     } else {
       const bool centre = e ? P::kCentreV : P::kCentreK;
-      reinterpret_cast<float4*>(smem + G::kScales + slot * (kTile * 16))[32 * e + lane] =
-          make_float4(sa, sb, centre ? fmaf(8.f, sa, za) : za, centre ? fmaf(8.f, sb, zb) : zb);
-      if (e) run_exp = max(run_exp, min(__reduce_max_sync(0xFFFFFFFFu, max(w.x << 16, w.y << 16)) >> 23, 254u));
+      const float ya = centre ? fmaf(8.f, sa, za) : za, yb = centre ? fmaf(8.f, sb, zb) : zb;
+      reinterpret_cast<float4*>(smem + G::kScales + slot * (kTile * 16))[32 * e + lane] = make_float4(sa, sb, ya, yb);
+      if (e) run_exp = max(run_exp, __reduce_max_sync(0xFFFFFFFFu, max(v_key_exp(sa, ya), v_key_exp(sb, yb))));
       if (lane == 0) tile.bad = INT_MAX;
     }
     if (lane == 0) (e ? tile.v_exp : tile.k_exp) = run_exp;
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   float o[HD / 2];  // of the row: columns hw HD / 2 .., dims hw HD / 4 .. and those HD / 2 further, in turn
 #pragma unroll
   for (int i = 0; i < HD / 2; ++i) o[i] = 0.f;
-  uint32_t v_exp = 41;
+  uint32_t v_exp = kLeastExp;
   auto add_part = [&](int i, const float* v) {  // 32 columns of a tile's O
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {

@@ -60,3 +60,16 @@ def test_a_query_that_is_not_finite_keeps_to_itself(dtype, bad):
         assert got[0, 2].isnan().all()
         keep = [0, 1, 3]
         _check_attention(got[:, keep], q64[:, keep], [(k64, v64)], [n - 2], [2], dtype, hd ** -0.5)
+
+
+@pytest.mark.parametrize("many", [False, True], ids=["few_rows_kernel", "many_rows_kernel"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_values_that_are_all_one_large_number(dtype, many):
+    """Rows of V without any range have the scale 0, so that nothing but their offset is of any size."""
+    rng = np.random.default_rng(52)
+    n, hd, large = 3000, 64, 2.0 ** (15 if dtype == "float16" else 60)
+    c, table, k64, v64 = _cache(rng.standard_normal((n, 1, hd)) * 0.1, np.full((n, 1, hd), -large), dtype)
+    new = 20 if many else 1
+    q, q64 = _to(rng.standard_normal((new, 4, hd)), dtype)
+    got = c.attention(q, _i32([n - new]), _wide(table, 64) if many else table)
+    (_check if many else _check_attention)(got, q64, [(k64, v64)], [n - new], [new], dtype, hd ** -0.5)
