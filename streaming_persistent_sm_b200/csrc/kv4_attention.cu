@@ -275,15 +275,15 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
   }
 
   // Running sums of the online softmax, all of them 2^-off times the true ones:
-  // off = m - (14 - exponent of V's largest scale so far, see v_key_exp), so that
-  // P s, which the second product takes in fp16, stays below 2^15 whatever the
-  // scales, and P y within fp32.
+  // off = m - 14, where m is at least a key's logit and its V's exponent together
+  // (v_key_exp, kSpread), for all keys so far.  So P s, which the second product
+  // takes in fp16, stays below 2^15 whatever the scales, and P y within fp32.
   float m = -INFINITY, off = 0.f;  // of row g
   F2 l2 = pair(0.f, 0.f), py2 = l2;  // l and the sum of p y, of this lane's keys only, in two halves
   float o[2 * WPL][4];               // rows 2t, 2t + 1: dims 4g + .. of both halves
 #pragma unroll
   for (int i = 0; i < 2 * WPL; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  uint32_t v_exp = kLeastExp;
+  uint32_t v_most = kLeastExp, v_least = 255;  // V's exponents so far (the least: of this lane's keys with a range)
   int cur = 0;
 #pragma unroll 1
   for (int step = first; step < n_steps; step += stride) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     // the step's scales as floats: lane 4 n + t's keys are 8 n + t and 8 n + 7 - t,
     // as S's columns have them; zeros for keys without a place (whatever the stage
     // held)
-    uint32_t e_top;
+    bool spread;
     {
       const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * kKeys * G::kRowBytes);
       const int ja = 8 * g + t, jb = 8 * g + 7 - t;
@@ -317,7 +317,10 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       scales[lane] = make_float4(s_of(ka), s_of(kb), z_of(ka, P::kCentreK), z_of(kb, P::kCentreK));
       const float4 vs = make_float4(s_of(va), s_of(vb), z_of(va, P::kCentreV), z_of(vb, P::kCentreV));
       scales[32 + lane] = vs;
-      e_top = __reduce_max_sync(0xFFFFFFFFu, max(v_key_exp(vs.x, vs.z), v_key_exp(vs.y, vs.w)));
+      const uint32_t ea = v_key_exp(vs.x, vs.z), eb = v_key_exp(vs.y, vs.w);
+      v_most = max(v_most, __reduce_max_sync(0xFFFFFFFFu, max(ea, eb)));
+      v_least = min(v_least, min(vs.x != 0.f ? ea : 255u, vs.y != 0.f ? eb : 255u));
+      spread = __any_sync(0xFFFFFFFFu, v_least + kSpread < v_most);
     }
     __syncwarp();
 
@@ -362,17 +365,26 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
     }
 
     // softmax of row g over the step's keys
-    float top = max3(x[0], x[1], x[2]);
+    float top;  // (sums rounded up, so that P does not pass its range however large the logits are)
+    if (!spread) {
+      top = max3(x[0], x[1], x[2]);
 #pragma unroll
-    for (int i = 3; i < 15; i += 2) top = max3(top, x[i], x[i + 1]);
-    top = fmaxf(top, x[15]);
+      for (int i = 3; i < 15; i += 2) top = max3(top, x[i], x[i + 1]);
+      top = __fadd_ru(fmaxf(top, x[15]), (float)((int)v_most - 127));
+    } else {
+      top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float4 vs = scales[32 + 4 * n + t];
+        top = max3(top, __fadd_ru(x[2 * n], (float)((int)v_key_exp(vs.x, vs.z) - 127)),
+                   __fadd_ru(x[2 * n + 1], (float)((int)v_key_exp(vs.y, vs.w) - 127)));
+      }
+    }
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const uint32_t e_new = max(v_exp, e_top);
     const float m_new = fmaxf(m, top);
-    if (__any_sync(0xFFFFFFFFu, m_new != m || e_new != v_exp)) {
-      // 14 + 127; rounded up, so that P does not pass its range however large the logits are
-      const float off_new = __fsub_ru(m_new == -INFINITY ? 0.f : m_new, (float)(141 - (int)e_new));
+    if (__any_sync(0xFFFFFFFFu, m_new != m)) {
+      const float off_new = __fsub_ru(m_new == -INFINITY ? 0.f : m_new, 14.f);
       const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
       l2 = mul2(l2, pair(fade, fade));  // a NaN stays
       py2 = mul2(py2, pair(fade, fade));
@@ -384,7 +396,6 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
       }
       m = m_new;
       off = off_new;
-      v_exp = e_new;
     }
     const F2 down = pair(-off, -off);
     if (!part) {

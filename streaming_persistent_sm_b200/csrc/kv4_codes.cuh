@@ -66,6 +66,14 @@ __device__ __forceinline__ uint32_t v_key_exp(float s, float y) {
   return max(max(min(es, 254u), ey == 255u ? 0u : ey - min(ey, 64u)), kLeastExp);  // a NaN says nothing
 }
 
+// A key's weight times its scale is an fp16 number of at most 2^15, and as long
+// as the exponent fields of the keys so far differ by no more than kSpread, their
+// largest stands for all: the product that counts most is then above 2^2, and
+// what the others lose below 2^-14 (2^-25 each) is nothing beside it.  Where they
+// differ by more, the bound follows each row's own largest product, so that a
+// value of no weight, or one that the row does not see, costs the others nothing.
+constexpr uint32_t kSpread = 12;
+
 // What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's
 // codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
 // that the output's rounding is off, relative, of random values).  fp16: Q to 22

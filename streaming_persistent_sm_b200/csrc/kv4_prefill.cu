@@ -70,6 +70,8 @@ struct PGeo {
 struct Tile {  // what its scales say
   uint32_t have;           // runs of 16 keys that have a place
   uint32_t k_exp, v_exp;   // biased exponents so far: V's largest scale (codes, see v_key_exp) or value, K's largest value
+  uint32_t v_least;        // V's least exponent so far, of keys with a range
+  bool spread;             // V's exponents differ by more than kSpread
   int bad;                 // values: the first key whose V is NaN
 };
 
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     if (!there || key0 + 2 * lane + 1 >= n_keys) w.y = 0;
     const float sa = __uint_as_float(w.x << 16), sb = __uint_as_float(w.y << 16);
     float za = __uint_as_float(w.x & 0xFFFF0000u), zb = __uint_as_float(w.y & 0xFFFF0000u);
+    uint32_t least = 255;
     if constexpr (G::kValues) {
       // the largest size of the values, a NaN left out
       const float ra = fmaxf(fmaxf(0.f, fabsf(za)), fabsf(fmaf(15.f, sa, za)));
@@ -241,10 +244,22 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       const bool centre = e ? P::kCentreV : P::kCentreK;
       const float ya = centre ? fmaf(8.f, sa, za) : za, yb = centre ? fmaf(8.f, sb, zb) : zb;
       reinterpret_cast<float4*>(smem + G::kScales + slot * (kTile * 16))[32 * e + lane] = make_float4(sa, sb, ya, yb);
-      if (e) run_exp = max(run_exp, __reduce_max_sync(0xFFFFFFFFu, max(v_key_exp(sa, ya), v_key_exp(sb, yb))));
+      if (e) {
+        const uint32_t ea = v_key_exp(sa, ya), eb = v_key_exp(sb, yb);
+        run_exp = max(run_exp, __reduce_max_sync(0xFFFFFFFFu, max(ea, eb)));
+        least = __reduce_min_sync(0xFFFFFFFFu, min(sa != 0.f ? ea : 255u, sb != 0.f ? eb : 255u));
+      }
       if (lane == 0) tile.bad = INT_MAX;
     }
+    if (e) {
+      if (j) least = min(least, tiles[(j - 1) & (2 * kRing - 1)].v_least);
+      if (lane == 0) {
+        tile.v_least = least;
+        tile.spread = least + kSpread < run_exp;
+      }
+    }
     if (lane == 0) (e ? tile.v_exp : tile.k_exp) = run_exp;
+    __syncwarp();  // the next tile's reads this one's record
   };
 
   // The first tiles' places and Q's values are under way together.
@@ -493,17 +508,27 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       for (int i = 0; i < 32; ++i)
         if (!((tile.have >> (2 * hw + (i >> 4))) & 1u) || key0 + 32 * hw + i > last) x[i] = -INFINITY;
     }
+    // (sums rounded up, so that P does not pass its range however large the logits are)
+    if (G::kValues || !tile.spread) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
+      for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
+      top *= k_tile;
+      if (!G::kValues) top = __fadd_ru(top, (float)((int)tile.v_exp - 127));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 vs = scales[32 + 16 * hw + i];
+        top = max3(top, __fadd_ru(x[2 * i] * k_tile, (float)((int)v_key_exp(vs.x, vs.z) - 127)),
+                   __fadd_ru(x[2 * i + 1] * k_tile, (float)((int)v_key_exp(vs.y, vs.w) - 127)));
+      }
+    }
     red[hw * kM + r] = top;
     bar_pair(1 + (warp & 3));  // the other half of the rows is the other warp's of the four
-    const float m_new = fmaxf(m, fmaxf(top, red[(hw ^ 1) * kM + r]) * k_tile);
+    const float m_new = fmaxf(m, fmaxf(top, red[(hw ^ 1) * kM + r]));
     const uint32_t v_new = tile.v_exp;
-    if (m_new != m || v_new != v_exp) {
-      // P reaches 2^15, as a weight or times V's largest scale; rounded up, so that
-      // it does not pass that however large the logits are
-      const float off_new =
-          __fsub_ru(m_new == -INFINITY ? 0.f : m_new, G::kValues ? 15.f : (float)(141 - (int)v_new));
+    if (m_new != m || (G::kValues && v_new != v_exp)) {
+      // P reaches 2^15, as a weight or times its key's V scale
+      const float off_new = __fsub_ru(m_new == -INFINITY ? 0.f : m_new, G::kValues ? 15.f : 14.f);
       const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
       // operands that are values shrink as the largest one grows
       const float o_fade = G::kValues ? fade * __uint_as_float(max(127 - (int)(v_new - v_exp), 0) << 23) : fade;

@@ -73,3 +73,59 @@ def test_values_that_are_all_one_large_number(dtype, many):
     q, q64 = _to(rng.standard_normal((new, 4, hd)), dtype)
     got = c.attention(q, _i32([n - new]), _wide(table, 64) if many else table)
     (_check if many else _check_attention)(got, q64, [(k64, v64)], [n - new], [new], dtype, hd ** -0.5)
+
+
+def _near(got, q64, k, v, past, dtype, scale):
+    """The bound of test_kv4_runs_gpu's _check for one sequence, and half of the type's least step: results below the
+    normal range (2^-14 for fp16) are multiples of it (2^-24), so their rounding is off by half of it however small
+    they are."""
+    torch = _torch()
+    info = torch.finfo(getattr(torch, dtype))
+    half = info.eps / 2
+    want, bulk, reach = R.attention(q64, k, v, past, scale)
+    logit = (2 * 2.0 ** -12 if dtype == "bfloat16" else 2.0 ** -22) + (q64.shape[-1] + 24) * 2.0 ** -24
+    weight = {"bfloat16": 2 * 2.0 ** -12, "float16": 2.0 ** -12, "float32": 2.0 ** -22}[dtype] + 1.01 * logit * (1 + reach)
+    tol = half * np.abs(want) + 2 * weight[..., None] * (bulk + np.abs(want)) * (1 + half) + info.smallest_normal * half
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (float((err - tol).max()), float(err.max()))
+
+
+KERNELS = [(d, m) for d in DTYPES for m in (False, True) if not (m and d == "bfloat16")]  # dtype, many rows
+HUGE = {"float32": 1e18, "bfloat16": 1e18, "float16": 1.5e4}
+TINY = {"float32": 1.0, "bfloat16": 1.0, "float16": 1e-6}
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype,many", KERNELS)
+def test_a_huge_value_changes_no_query_that_does_not_weigh_it(dtype, hd, many):
+    """The values of tokens 70 and 100 are huge.  Queries before them do not see them; those behind see their keys
+    at logits some 60 below the others', so that they weigh 1e-26."""
+    rng = np.random.default_rng(53)
+    n, group = 140, 2
+    u = rng.choice([-1.0, 1.0], hd)
+    k = rng.standard_normal((n, 1, hd)) * 0.1
+    v = rng.standard_normal((n, 1, hd)) * TINY[dtype]
+    k[[70, 100], 0] = -60.0 * hd ** -0.5 * u
+    v[[70, 100]] *= HUGE[dtype] / TINY[dtype]
+    q, q64 = _to(u + 0.1 * rng.standard_normal((n, group, hd)), dtype)
+    c, table, k64, v64 = _cache(k, v, dtype)
+    got = c.attention(q, _i32([0]), _wide(table, 64) if many else table)
+    _near(got, q64, k64, v64, 0, dtype, hd ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,many", KERNELS)
+def test_a_huge_value_fades_when_larger_logits_come(dtype, many):
+    """A huge value of weight 1 among the first keys, whose logits the later keys pass by 60: what it weighs then is
+    nothing, and the small values behind it, up to a second huge one of weight nothing, are the answer."""
+    rng = np.random.default_rng(54)
+    n, hd = 1500, 64
+    u = rng.choice([-1.0, 1.0], hd)
+    k = rng.standard_normal((n, 1, hd)) * 0.1 + np.where(np.arange(n) < 300, -60.0 * hd ** -0.5, 0.0)[:, None, None] * u
+    v = rng.standard_normal((n, 1, hd)) * TINY[dtype]
+    v[[3, 700]] *= HUGE[dtype] / TINY[dtype]
+    k[700] = -120.0 * hd ** -0.5 * u
+    new = 20 if many else 1
+    q, q64 = _to(u + 0.1 * rng.standard_normal((new, 4, hd)), dtype)
+    c, table, k64, v64 = _cache(k, v, dtype)
+    got = c.attention(q, _i32([n - new]), _wide(table, 64) if many else table)
+    _near(got, q64, k64, v64, n - new, dtype, hd ** -0.5)
