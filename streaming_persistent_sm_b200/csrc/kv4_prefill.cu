@@ -8,7 +8,8 @@
 // of V is MN-major: nothing is transposed.  What the operands hold depends on what
 // the type has to keep:
 //  * bf16: the values s c + z rounded to fp16 (2^-12, as Q and P), times a power of
-//    two that follows the largest value so far;
+//    two that follows K's largest value in the tile (each key's own, where they differ
+//    much) and V's largest so far;
 //  * fp16, fp32: the codes, which are exact (odd nibbles at 16 times their value);
 //    scales and offsets enter per key around the products, as for few rows.
 // S goes to TMEM; two threads a row (32 keys each) turn it into P, in TMEM too,
@@ -43,6 +44,7 @@ constexpr int kTile = 64;      // keys of a tile
 constexpr int kThreadsP = 256;
 constexpr int kSplits = 8;
 constexpr int kRing = 4;       // tiles in staging
+constexpr uint32_t kLeastK = 15;  // K's exponents: both 2^(141 - field) and its inverse are normal numbers
 
 template <typename T, int HD>
 struct PGeo {
@@ -58,7 +60,8 @@ struct PGeo {
   static constexpr int kStage = 2 * kCodes + kTile * 8;
   static constexpr int kScales = kOps + kRing * kStage;       // what a tile's scales become, 1 KB each
   static constexpr int kRed = kScales + kRing * kTile * 16;   // [2][kM] floats: both threads of a row
-  static constexpr int kBytes = kRed + 2 * kM * 4;
+  static constexpr int kFactors = kRed + 2 * kM * 4;          // values: what each key of a tile was divided by
+  static constexpr int kBytes = kFactors + (P::kBf16 ? kRing * kTile * 4 : 0);
   // after the keys: O [kM][HD], offsets, sums
   static constexpr int kJoin = kM * (HD + 2) * 4;
   static constexpr int kSmem = (kBytes > kJoin ? kBytes : kJoin) + 1024;  // and what aligns it
@@ -69,7 +72,8 @@ struct PGeo {
 
 struct Tile {  // what its scales say
   uint32_t have;           // runs of 16 keys that have a place
-  uint32_t k_exp, v_exp;   // biased exponents so far: V's largest scale (codes, see v_key_exp) or value, K's largest value
+  uint32_t k_exp, v_exp;   // biased exponents: K's largest value here; V's largest scale (codes, see v_key_exp) or value so far
+  bool k_spread;           // values: K's exponents differ by more than kSpread, each key has its own
   uint32_t v_least;        // V's least exponent so far, of keys with a range
   bool spread;             // V's exponents differ by more than kSpread
   int bad;                 // values: the first key whose V is NaN
@@ -226,8 +230,25 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       // the largest size of the values, a NaN left out
       const float ra = fmaxf(fmaxf(0.f, fabsf(za)), fabsf(fmaf(15.f, sa, za)));
       const float rb = fmaxf(fmaxf(0.f, fabsf(zb)), fabsf(fmaf(15.f, sb, zb)));
-      run_exp = max(run_exp, min(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(ra, rb))) >> 23, 254u));
-      const float f = __uint_as_float((268u - run_exp) << 23);  // the largest value to 2^14..2^15
+      uint32_t ea = min(__float_as_uint(ra) >> 23, 254u), eb = min(__float_as_uint(rb) >> 23, 254u);
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(ea, eb));
+      if (e == 0) {
+        // K's product is taken tile by tile, so it has a power of two for each; keys
+        // that differ by more than kSpread have one each, which S's columns take back
+        run_exp = max(top, kLeastK);
+        const bool spread =
+            __any_sync(0xFFFFFFFFu, (ra > 0.f && ea + kSpread < run_exp) || (rb > 0.f && eb + kSpread < run_exp));
+        ea = spread ? max(ea, kLeastK) : run_exp;
+        eb = spread ? max(eb, kLeastK) : run_exp;
+        if (spread)
+          reinterpret_cast<float2*>(smem + G::kFactors + slot * (kTile * 4))[lane] =
+              make_float2(__uint_as_float((ea - 14u) << 23), __uint_as_float((eb - 14u) << 23));
+        if (lane == 0) tile.k_spread = spread;
+      } else {
+        ea = eb = run_exp = max(run_exp, top);
+      }
+      // the largest value to 2^14..2^15
+      const float fa = __uint_as_float((268u - ea) << 23), fb = __uint_as_float((268u - eb) << 23);
       if (e) {  // a NaN must not reach rows that do not see it
         const int bad = (int)__reduce_min_sync(0xFFFFFFFFu, za != za ? 2 * lane : zb != zb ? 2 * lane + 1 : INT_MAX);
         if (lane == 0) tile.bad = bad;
@@ -239,7 +260,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
         return *reinterpret_cast<const uint32_t*>(&h);
       };
       reinterpret_cast<uint4*>(smem + G::kScales + slot * (kTile * 16))[32 * e + lane] =
-          make_uint4(twice(sa * f), twice(za * f), twice(sb * f), twice(zb * f));
+          make_uint4(twice(sa * fa), twice(za * fa), twice(sb * fb), twice(zb * fb));
     } else {
       const bool centre = e ? P::kCentreV : P::kCentreK;
       const float ya = centre ? fmaf(8.f, sa, za) : za, yb = centre ? fmaf(8.f, sb, zb) : zb;
@@ -488,9 +509,20 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     } else {
       tmem_ld16x2(mine + G::kS + 32 * hw, x);
     }
-    // > 0, so that a logit of -infinity stays one
-    const float k_tile =
-        G::kValues ? fmaxf(k_mul * __uint_as_float((tile.k_exp - 14u) << 23), __uint_as_float(1u)) : k_mul;
+    float k_tile = k_mul;
+    if constexpr (G::kValues) {
+      if (tile.k_spread) {
+        const float4* f = reinterpret_cast<const float4*>(smem + G::kFactors + (j & (kRing - 1)) * (kTile * 4)) + 8 * hw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 w = f[i];
+          x[4 * i] *= w.x, x[4 * i + 1] *= w.y, x[4 * i + 2] *= w.z, x[4 * i + 3] *= w.w;
+        }
+      } else {
+        // > 0, so that a logit of -infinity stays one
+        k_tile = fmaxf(k_mul * __uint_as_float((tile.k_exp - 14u) << 23), __uint_as_float(1u));
+      }
+    }
     float top = -INFINITY;
     if constexpr (!G::kValues) {
       const F2 z2 = pair(z_mul, z_mul);

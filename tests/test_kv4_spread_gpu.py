@@ -129,3 +129,22 @@ def test_a_huge_value_fades_when_larger_logits_come(dtype, many):
     c, table, k64, v64 = _cache(k, v, dtype)
     got = c.attention(q, _i32([n - new]), _wide(table, 64) if many else table)
     _near(got, q64, k64, v64, n - new, dtype, hd ** -0.5)
+
+
+@pytest.mark.parametrize("many", [False, True], ids=["few_rows_kernel", "many_rows_kernel"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_a_huge_key_changes_no_query_that_does_not_weigh_it(dtype, hd, many):
+    """The keys of tokens 70 and 100 are huge.  Queries before them do not see them; those behind see them at logits
+    of -1e13 and less, so their exact weights are zeros and the answers are those without these tokens."""
+    rng = np.random.default_rng(55)
+    n, group, at = 140, 2, [70, 100]
+    u = rng.choice([-1.0, 1.0], hd)
+    k = rng.standard_normal((n, 1, hd))
+    k[at, 0] = -1e13 * u
+    v = rng.standard_normal((n, 1, hd))
+    q, q64 = _to(u + 0.1 * rng.standard_normal((n, group, hd)), dtype)
+    c, table, k64, v64 = _cache(k, v, dtype)
+    got = c.attention(q, _i32([0]), _wide(table, 64) if many else table)
+    there = np.setdiff1d(np.arange(n), at)
+    _near(got[there], q64[there], k64[there], v64[there], 0, dtype, hd ** -0.5)
