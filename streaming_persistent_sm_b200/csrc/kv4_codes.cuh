@@ -72,6 +72,9 @@ __device__ __forceinline__ uint32_t v_key_exp(float s, float y) {
 // what the others lose below 2^-14 (2^-25 each) is nothing beside it.  Where they
 // differ by more, the bound follows each row's own largest product, so that a
 // value of no weight, or one that the row does not see, costs the others nothing.
+// Operands that hold values (bf16, many rows) have one power of two for all keys,
+// or one for each, by the same rule: 2^12 below the largest, which stands at 2^15
+// at most, a value keeps all of fp16's digits.
 constexpr uint32_t kSpread = 12;
 
 // What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's

@@ -8,8 +8,8 @@
 // of V is MN-major: nothing is transposed.  What the operands hold depends on what
 // the type has to keep:
 //  * bf16: the values s c + z rounded to fp16 (2^-12, as Q and P), times a power of
-//    two that follows K's largest value in the tile (each key's own, where they differ
-//    much) and V's largest so far;
+//    two that follows K's largest value in the tile and V's largest so far (each
+//    key's own, where they differ much);
 //  * fp16, fp32: the codes, which are exact (odd nibbles at 16 times their value);
 //    scales and offsets enter per key around the products, as for few rows.
 // S goes to TMEM; two threads a row (32 keys each) turn it into P, in TMEM too,
@@ -60,8 +60,8 @@ struct PGeo {
   static constexpr int kStage = 2 * kCodes + kTile * 8;
   static constexpr int kScales = kOps + kRing * kStage;       // what a tile's scales become, 1 KB each
   static constexpr int kRed = kScales + kRing * kTile * 16;   // [2][kM] floats: both threads of a row
-  static constexpr int kFactors = kRed + 2 * kM * 4;          // values: what each key of a tile was divided by
-  static constexpr int kBytes = kFactors + (P::kBf16 ? kRing * kTile * 4 : 0);
+  static constexpr int kFactors = kRed + 2 * kM * 4;          // values: what K's keys were divided by, V's exponents
+  static constexpr int kBytes = kFactors + (P::kBf16 ? kRing * 2 * kTile * 4 : 0);
   // after the keys: O [kM][HD], offsets, sums
   static constexpr int kJoin = kM * (HD + 2) * 4;
   static constexpr int kSmem = (kBytes > kJoin ? kBytes : kJoin) + 1024;  // and what aligns it
@@ -74,7 +74,6 @@ struct Tile {  // what its scales say
   uint32_t have;           // runs of 16 keys that have a place
   uint32_t k_exp, v_exp;   // biased exponents: K's largest value here; V's largest scale (codes, see v_key_exp) or value so far
   bool k_spread;           // values: K's exponents differ by more than kSpread, each key has its own
-  uint32_t v_least;        // V's least exponent so far, of keys with a range
   bool spread;             // V's exponents differ by more than kSpread
   int bad;                 // values: the first key whose V is NaN
 };
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
 
   // What the operands and the softmax need of a tile's scales, two keys a lane, of
   // K (e = 0) or V; zeros for keys without a place.
-  uint32_t run_exp = kLeastExp;
+  uint32_t run_exp = kLeastExp, run_least = 255;  // (the least: of this lane's keys with a range)
   auto prepare = [&](int j, int e) {
     if (j >= n_mine) return;
     arrived(j);
@@ -225,7 +224,6 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     if (!there || key0 + 2 * lane + 1 >= n_keys) w.y = 0;
     const float sa = __uint_as_float(w.x << 16), sb = __uint_as_float(w.y << 16);
     float za = __uint_as_float(w.x & 0xFFFF0000u), zb = __uint_as_float(w.y & 0xFFFF0000u);
-    uint32_t least = 255;
     if constexpr (G::kValues) {
       // the largest size of the values, a NaN left out
       const float ra = fmaxf(fmaxf(0.f, fabsf(za)), fabsf(fmaf(15.f, sa, za)));
@@ -241,11 +239,21 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
         ea = spread ? max(ea, kLeastK) : run_exp;
         eb = spread ? max(eb, kLeastK) : run_exp;
         if (spread)
-          reinterpret_cast<float2*>(smem + G::kFactors + slot * (kTile * 4))[lane] =
+          reinterpret_cast<float2*>(smem + G::kFactors + slot * (2 * kTile * 4))[lane] =
               make_float2(__uint_as_float((ea - 14u) << 23), __uint_as_float((eb - 14u) << 23));
         if (lane == 0) tile.k_spread = spread;
       } else {
-        ea = eb = run_exp = max(run_exp, top);
+        // V's follows the largest value so far; where the exponents so far differ by
+        // more than kSpread, each key has its own, which the weights take back
+        run_exp = max(run_exp, top);
+        run_least = min(run_least, min(ra > 0.f ? ea : 255u, rb > 0.f ? eb : 255u));
+        const bool spread = __any_sync(0xFFFFFFFFu, run_least + kSpread < run_exp);
+        if (lane == 0) tile.spread = spread;
+        ea = spread ? max(ea, kLeastExp) : run_exp;
+        eb = spread ? max(eb, kLeastExp) : run_exp;
+        if (spread)
+          reinterpret_cast<float2*>(smem + G::kFactors + slot * (2 * kTile * 4) + kTile * 4)[lane] =
+              make_float2((float)ea, (float)eb);
       }
       // the largest value to 2^14..2^15
       const float fa = __uint_as_float((268u - ea) << 23), fb = __uint_as_float((268u - eb) << 23);
@@ -268,19 +276,13 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       if (e) {
         const uint32_t ea = v_key_exp(sa, ya), eb = v_key_exp(sb, yb);
         run_exp = max(run_exp, __reduce_max_sync(0xFFFFFFFFu, max(ea, eb)));
-        least = __reduce_min_sync(0xFFFFFFFFu, min(sa != 0.f ? ea : 255u, sb != 0.f ? eb : 255u));
+        run_least = min(run_least, min(sa != 0.f ? ea : 255u, sb != 0.f ? eb : 255u));
+        const bool spread = __any_sync(0xFFFFFFFFu, run_least + kSpread < run_exp);
+        if (lane == 0) tile.spread = spread;
       }
       if (lane == 0) tile.bad = INT_MAX;
     }
-    if (e) {
-      if (j) least = min(least, tiles[(j - 1) & (2 * kRing - 1)].v_least);
-      if (lane == 0) {
-        tile.v_least = least;
-        tile.spread = least + kSpread < run_exp;
-      }
-    }
     if (lane == 0) (e ? tile.v_exp : tile.k_exp) = run_exp;
-    __syncwarp();  // the next tile's reads this one's record
   };
 
   // The first tiles' places and Q's values are under way together.
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   float o[HD / 2];  // of the row: columns hw HD / 2 .., dims hw HD / 4 .. and those HD / 2 further, in turn
 #pragma unroll
   for (int i = 0; i < HD / 2; ++i) o[i] = 0.f;
-  uint32_t v_exp = kLeastExp;
+  int v_exp = (int)kLeastExp;  // values: O stands at 2^(141 - v_exp)
   auto add_part = [&](int i, const float* v) {  // 32 columns of a tile's O
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     float k_tile = k_mul;
     if constexpr (G::kValues) {
       if (tile.k_spread) {
-        const float4* f = reinterpret_cast<const float4*>(smem + G::kFactors + (j & (kRing - 1)) * (kTile * 4)) + 8 * hw;
+        const float4* f = reinterpret_cast<const float4*>(smem + G::kFactors + (j & (kRing - 1)) * (2 * kTile * 4)) + 8 * hw;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float4 w = f[i];
@@ -557,13 +559,35 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     red[hw * kM + r] = top;
     bar_pair(1 + (warp & 3));  // the other half of the rows is the other warp's of the four
     const float m_new = fmaxf(m, fmaxf(top, red[(hw ^ 1) * kM + r]));
-    const uint32_t v_new = tile.v_exp;
-    if (m_new != m || (G::kValues && v_new != v_exp)) {
+    const float* v_own = reinterpret_cast<const float*>(smem + G::kFactors + (j & (kRing - 1)) * (2 * kTile * 4)) +
+                         kTile + 32 * hw;  // values: V's exponents, where they are spread
+    const bool spread = G::kValues && tile.spread;
+    if (m_new != m || spread || (G::kValues && (int)tile.v_exp != v_exp)) {
       // P reaches 2^15, as a weight or times its key's V scale
       const float off_new = __fsub_ru(m_new == -INFINITY ? 0.f : m_new, G::kValues ? 15.f : 14.f);
       const float fade = m == -INFINITY ? 0.f : ex2(off - off_new);
-      // operands that are values shrink as the largest one grows
-      const float o_fade = G::kValues ? fade * __uint_as_float(max(127 - (int)(v_new - v_exp), 0) << 23) : fade;
+      float o_fade = fade;
+      if constexpr (G::kValues) {
+        int v_new = (int)tile.v_exp;
+        if (spread) {
+          // The row's own exponent: P is the weight times 2^(its key's exponent - v_new),
+          // at most 2^15.  Down with the fading of what O holds, so that O only shrinks.
+          float most = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            most = max3(most, __fadd_ru(fmaf(x[i], k_tile, -off_new), v_own[i]),
+                        __fadd_ru(fmaf(x[i + 1], k_tile, -off_new), v_own[i + 1]));
+          bar_pair(1 + (warp & 3));  // the other has read this row's largest logit
+          red[hw * kM + r] = most;
+          bar_pair(1 + (warp & 3));
+          most = fmaxf(fmaxf(most, red[(hw ^ 1) * kM + r]), -1024.f);
+          v_new = max((int)ceilf(most) - 15, (int)kLeastExp);
+          if (m != -INFINITY) v_new = max(v_new, v_exp - (int)fminf(off_new - off, 512.f));
+        }
+        // operands that are values shrink as the exponent grows
+        o_fade = m == -INFINITY ? 0.f : ex2((off - off_new) + (float)(v_exp - v_new));
+        v_exp = v_new;
+      }
       const F2 f2 = pair(fade, fade), o2 = pair(o_fade, o_fade);
       l2 = mul2(l2, f2);  // a NaN stays
       if (!G::kValues) py2 = mul2(py2, f2);
@@ -575,7 +599,6 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       }
       m = m_new;
       off = off_new;
-      v_exp = v_new;
     }
     if (tile.bad <= last - key0) l2 = pair(NAN, NAN);  // `last` is -1 for rows without a key
     const F2 down = pair(-off, -off), k2 = pair(k_tile, k_tile);
@@ -590,7 +613,12 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
         const F2 p = pair(pf.x, pf.y);
         l2 = add2(l2, p);
         if constexpr (G::kValues) {
-          hi[i] = pack_f16(pf.x, pf.y);
+          if (spread) {
+            const float2 e = *reinterpret_cast<const float2*>(v_own + 2 * n);
+            hi[i] = pack_f16(ex2(d.x + (e.x - (float)v_exp)), ex2(d.y + (e.y - (float)v_exp)));
+          } else {
+            hi[i] = pack_f16(pf.x, pf.y);
+          }
           continue;
         }
         const float4 vs = scales[32 + 16 * hw + n];
@@ -647,7 +675,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     // codes: odd nibbles stand 16 times as high, raw ones at 2^-24; values at
     // 2^14 / 2^v_exp, their weights at 2^15
     constexpr float even = P::kCentreV ? 1.f : 16777216.f;
-    const float back = __uint_as_float(v_exp - 29u << 23);
+    const float back = __uint_as_float((uint32_t)(v_exp - 29) << 23);
 #pragma unroll
     for (int i = 0; i < HD / 2; ++i)
       o[i] = G::kValues ? o[i] * back : fmaf(o[i], i >> 1 & 1 ? even * 0.0625f : even, py);
