@@ -103,14 +103,16 @@ struct PrefillArgs {
   float scale_log2;
 };
 
-// Waits for a phase of a barrier; false after a second (nothing but a lost copy or
-// product would take so long): the rows then answer NaN.
+// Waits for a phase of a barrier; false where it has not ended after a second, nor
+// when looked at once more (a context that was switched out comes back late).
+// Nothing but a lost copy or product takes so long: the block then starts nothing
+// more and its rows answer NaN.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (globaltimer() - t0 < 1000000000ull)
     if (mbar_try_wait(bar, parity)) return true;
-  return false;
+  return mbar_try_wait(bar, parity);
 }
 
 // 32 columns of a thread's TMEM lane at two addresses each, waited for together.
@@ -136,6 +138,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   __shared__ __align__(8) uint64_t bars[2 + kRing];  // S ready, O ready, codes of a tile here
   __shared__ Tile tiles[2 * kRing];  // a tile is copied before the one four earlier is done with
   __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_lost[2];  // a wait before the barrier of an even (odd) tile has not ended
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hw = warp >> 2;                    // half of the keys (S columns), and of the dims (O columns)
@@ -166,6 +169,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   const int n_mine = n_tiles > rank ? (n_tiles - rank + a.split - 1) / a.split : 0;  // every split-th tile
 
   if (tid == 0) {
+    s_lost[0] = s_lost[1] = 0;
     for (int i = 0; i < 2 + kRing; ++i) mbar_init(&bars[i], i < 2 ? 1 : 4);
     fence_mbar_init();
   }
@@ -206,15 +210,19 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       }
     }
   };
-  bool ok = true;
-  auto arrived = [&](int j) { ok = ok && wait_bounded(&bars[2 + (j & (kRing - 1))], (j / kRing) & 1); };
+  // `turn`: the tile whose barrier comes next (-1: the one before the first tile).
+  // Flags are read behind their barrier, while waits behind it set the other one.
+  auto await = [&](uint64_t* bar, int phase, int turn) {
+    if (!wait_bounded(bar, phase & 1)) s_lost[turn & 1] = 1;
+  };
+  auto arrived = [&](int j, int turn) { await(&bars[2 + (j & (kRing - 1))], j / kRing, turn); };
 
   // What the operands and the softmax need of a tile's scales, two keys a lane, of
   // K (e = 0) or V; zeros for keys without a place.
   uint32_t run_exp = kLeastExp, run_least = 255;  // (the least: of this lane's keys with a range)
-  auto prepare = [&](int j, int e) {
+  auto prepare = [&](int j, int e, int turn) {
     if (j >= n_mine) return;
-    arrived(j);
+    arrived(j, turn);
     const int slot = j & (kRing - 1), key0 = (rank + j * a.split) * kTile;
     Tile& tile = tiles[j & (2 * kRing - 1)];
     uint2 w = *reinterpret_cast<const uint2*>(smem + G::kOps + slot * G::kStage + 2 * G::kCodes + e * (4 * kTile) +
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   __syncthreads();
   tc_fence_after();
   if (warp >> 1 == 1)
-    for (int j = 0; j < 2; ++j) prepare(j, warp & 1);
+    for (int j = 0; j < 2; ++j) prepare(j, warp & 1, -1);
   __syncthreads();
   const uint32_t tmem = s_tmem, mine = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t smem0 = smem_u32(smem);
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   };
   // adds a tile's O but for its last 32 columns, whose address it gives
   auto add_o = [&](int j) -> uint32_t {
-    ok = ok && wait_bounded(&bars[1], j & 1);
+    await(&bars[1], j, j + 1);
     tc_fence_after();
     if (HD == 128) {
       float v[32];
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
   };
   // K's and V's words of a key to 16-byte units of its rows, two or four a thread
   auto expand = [&](int j) {
-    arrived(j);
+    arrived(j, j - 1);
     const int slot = j & (kRing - 1);
     const uint8_t* stage = smem + G::kOps + slot * G::kStage;
     const int key = tid >> 2, part = tid & 3;
@@ -485,21 +493,24 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     __syncthreads();
     if (tid == 0) issue_s(0);
     if (warp >= 4) {
-      copy(kRing);
+      if (!s_lost[1]) copy(kRing);
       look_up(kRing + 1);
     }
-    if (warp >> 1 == 1) prepare(2, warp & 1);
+    if (warp >> 1 == 1) prepare(2, warp & 1, 0);
   }
+  int j = 0;
 #pragma unroll 1
-  for (int j = 0; j < n_mine; ++j) {
+  for (; j < n_mine; ++j) {
+    const int lost = s_lost[(j + 1) & 1];
     // While S of this tile and O of the one before are computed, the next tile is
     // expanded.
     const int key0 = (rank + j * a.split) * kTile;
     if (j + 1 < n_mine) expand(j + 1);
+    if (lost) break;
     const uint32_t rest = j ? add_o(j - 1) : 0u;
     const Tile tile = tiles[j & (2 * kRing - 1)];
     const float4* scales = reinterpret_cast<const float4*>(smem + G::kScales + (j & (kRing - 1)) * (kTile * 16));
-    ok = ok && wait_bounded(&bars[0], j & 1);
+    await(&bars[0], j, j);
     tc_fence_after();
 
     // the row's logits of 32 keys, k_tile times them in units of log2
@@ -641,10 +652,10 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     __syncthreads();
     tc_fence_after();
     if (warp >= 4) {
-      copy(j + 1 + kRing);  // where the tile was that is expanded now
+      if (!s_lost[j & 1]) copy(j + 1 + kRing);  // where the tile was that is expanded now
       look_up(j + 2 + kRing);
     } else if (warp >= 2)
-      prepare(j + 3, warp & 1);
+      prepare(j + 3, warp & 1, j + 1);
     else if (lane == 0) {
       if (warp == 1)
         issue_o(j);
@@ -653,13 +664,17 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     }
     __syncwarp();
   }
-  if (n_mine) {
+  if (j < n_mine) {  // given up: what was started (copies of the next tiles, S, the O before) ends before its memory is left
+    for (int i = j; i < min(n_mine, j + kRing); ++i) arrived(i, j);
+    await(&bars[0], j, j);
+    if (j) await(&bars[1], j - 1, j);
+  } else if (n_mine) {
     float v[32];
     tmem_ld16x2(add_o(n_mine - 1), v);
     add_part(HD / 2 - 32, v);
     tc_fence_before();
   }
-  ok = __syncthreads_and(ok);
+  __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, G::kCols);
   // a thread of each half holds its dims of the row; the sums come together
   {
@@ -680,7 +695,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     for (int i = 0; i < HD / 2; ++i)
       o[i] = G::kValues ? o[i] * back : fmaf(o[i], i >> 1 & 1 ? even * 0.0625f : even, py);
     const float sum = G::kValues ? l * 0x1p-15f : l;
-    const float none = ok ? 0.f : NAN;
+    const float none = s_lost[0] || s_lost[1] ? NAN : 0.f;
     float* join = reinterpret_cast<float*>(smem);  // [kM][HD + 2]
     if (a.split == 1) {
       if (my_row < rows) {
