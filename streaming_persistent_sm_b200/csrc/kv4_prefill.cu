@@ -129,6 +129,45 @@ __device__ __forceinline__ void tmem_ld32_two(uint32_t at_a, float* a, uint32_t 
 
 __device__ __forceinline__ void bar_pair(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
+// What a tile takes besides where its keys' exponents are spread, for a thread's 32
+// keys.  Out of line, on a copy of x: within the loop over tiles their code costs the
+// tiles that do without it 4 us of 234.
+struct Logits {
+  float x[32];
+};
+// K's keys have been divided by f each.
+__device__ __noinline__ void multiply_keys(Logits* at, const float* f) {
+#pragma unroll 4
+  for (int i = 0; i < 32; ++i) at->x[i] *= f[i];
+}
+// The largest logit with its key's V exponent (rounded up); scales of V, two keys each.
+__device__ __noinline__ float largest_product(const Logits* at, float k_tile, const float4* scales) {
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i)
+    top = max3(top, __fadd_ru(at->x[2 * i] * k_tile, (float)((int)v_key_exp(scales[i].x, scales[i].z) - 127)),
+               __fadd_ru(at->x[2 * i + 1] * k_tile, (float)((int)v_key_exp(scales[i].y, scales[i].w) - 127)));
+  return top;
+}
+// Values: the largest of the weights' logarithms with their keys' exponents.
+__device__ __noinline__ float largest_weight(const Logits* at, float k_tile, float off, const float* v_own) {
+  float most = -1024.f;
+#pragma unroll 4
+  for (int i = 0; i < 32; ++i) most = fmaxf(most, __fadd_ru(fmaf(at->x[i], k_tile, -off), v_own[i]));
+  return most;
+}
+// The weights' sum; x becomes the logarithms of P, which are times 2^(their keys' exponents - v_exp).
+__device__ __noinline__ float sum_weights(Logits* at, float k_tile, float off, const float* v_own, int v_exp) {
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < 32; ++i) {
+    const float d = fmaf(at->x[i], k_tile, -off);
+    sum += ex2(d);
+    at->x[i] = d + (v_own[i] - (float)v_exp);
+  }
+  return sum;
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     kv4_prefill_kernel(const Kv4Dev c, const T* __restrict__ q, T* __restrict__ out, const PrefillArgs a) {
@@ -525,12 +564,11 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
     float k_tile = k_mul;
     if constexpr (G::kValues) {
       if (tile.k_spread) {
-        const float4* f = reinterpret_cast<const float4*>(smem + G::kFactors + (j & (kRing - 1)) * (2 * kTile * 4)) + 8 * hw;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 w = f[i];
-          x[4 * i] *= w.x, x[4 * i + 1] *= w.y, x[4 * i + 2] *= w.z, x[4 * i + 3] *= w.w;
-        }
+        Logits copy;
+        for (int i = 0; i < 32; ++i) copy.x[i] = x[i];
+        multiply_keys(&copy, reinterpret_cast<const float*>(smem + G::kFactors + (j & (kRing - 1)) * (2 * kTile * 4)) +
+                                 32 * hw);
+        for (int i = 0; i < 32; ++i) x[i] = copy.x[i];
       } else {
         // > 0, so that a logit of -infinity stays one
         k_tile = fmaxf(k_mul * __uint_as_float((tile.k_exp - 14u) << 23), __uint_as_float(1u));
@@ -560,12 +598,9 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       top *= k_tile;
       if (!G::kValues) top = __fadd_ru(top, (float)((int)tile.v_exp - 127));
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float4 vs = scales[32 + 16 * hw + i];
-        top = max3(top, __fadd_ru(x[2 * i] * k_tile, (float)((int)v_key_exp(vs.x, vs.z) - 127)),
-                   __fadd_ru(x[2 * i + 1] * k_tile, (float)((int)v_key_exp(vs.y, vs.w) - 127)));
-      }
+      Logits copy;
+      for (int i = 0; i < 32; ++i) copy.x[i] = x[i];
+      top = largest_product(&copy, k_tile, scales + 32 + 16 * hw);
     }
     red[hw * kM + r] = top;
     bar_pair(1 + (warp & 3));  // the other half of the rows is the other warp's of the four
@@ -583,15 +618,13 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
         if (spread) {
           // The row's own exponent: P is the weight times 2^(its key's exponent - v_new),
           // at most 2^15.  Down with the fading of what O holds, so that O only shrinks.
-          float most = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            most = max3(most, __fadd_ru(fmaf(x[i], k_tile, -off_new), v_own[i]),
-                        __fadd_ru(fmaf(x[i + 1], k_tile, -off_new), v_own[i + 1]));
+          Logits copy;
+          for (int i = 0; i < 32; ++i) copy.x[i] = x[i];
+          float most = largest_weight(&copy, k_tile, off_new, v_own);
           bar_pair(1 + (warp & 3));  // the other has read this row's largest logit
           red[hw * kM + r] = most;
           bar_pair(1 + (warp & 3));
-          most = fmaxf(fmaxf(most, red[(hw ^ 1) * kM + r]), -1024.f);
+          most = fmaxf(most, red[(hw ^ 1) * kM + r]);
           v_new = max((int)ceilf(most) - 15, (int)kLeastExp);
           if (m != -INFINITY) v_new = max(v_new, v_exp - (int)fminf(off_new - off, 512.f));
         }
@@ -611,8 +644,15 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       m = m_new;
       off = off_new;
     }
-    if (tile.bad <= last - key0) l2 = pair(NAN, NAN);  // `last` is -1 for rows without a key
-    const F2 down = pair(-off, -off), k2 = pair(k_tile, k_tile);
+    F2 down = pair(-off, -off), k2 = pair(k_tile, k_tile), l_own = l2;
+    if (spread) {
+      Logits copy;
+      for (int i = 0; i < 32; ++i) copy.x[i] = x[i];
+      l_own = add2(l2, pair(sum_weights(&copy, k_tile, off, v_own, v_exp), 0.f));
+      for (int i = 0; i < 32; ++i) x[i] = copy.x[i];
+      k2 = pair(1.f, 1.f);
+      down = pair(0.f, 0.f);
+    }
 #pragma unroll
     for (int g = 0; g < 2; ++g) {  // 16 keys: 8 columns of P
       uint32_t hi[8], lo[8];
@@ -624,12 +664,7 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
         const F2 p = pair(pf.x, pf.y);
         l2 = add2(l2, p);
         if constexpr (G::kValues) {
-          if (spread) {
-            const float2 e = *reinterpret_cast<const float2*>(v_own + 2 * n);
-            hi[i] = pack_f16(ex2(d.x + (e.x - (float)v_exp)), ex2(d.y + (e.y - (float)v_exp)));
-          } else {
-            hi[i] = pack_f16(pf.x, pf.y);
-          }
+          hi[i] = pack_f16(pf.x, pf.y);
           continue;
         }
         const float4 vs = scales[32 + 16 * hw + n];
@@ -647,6 +682,8 @@ __global__ void __launch_bounds__(kThreadsP, PGeo<T, HD>::kPerSm)
       tmem_st8(mine + G::kP + 16 * hw + 8 * g, hi);
       if (P::kPLow) tmem_st8(mine + G::kP + 32 + 16 * hw + 8 * g, lo);
     }
+    if (spread) l2 = l_own;
+    if (tile.bad <= last - key0) l2 = pair(NAN, NAN);  // `last` is -1 for rows without a key
     tmem_st_wait();
     tc_fence_before();
     __syncthreads();
