@@ -59,8 +59,8 @@ constexpr int kMaxSplit = 16;
 constexpr int kManyRows = 64;
 constexpr int64_t kManyWork = 1 << 20;
 bool many_rows(const Kv4Dev& d, int64_t rows) {
-  return rows >= kManyRows && (rows + 7) / 8 * d.n_kv * d.batch >=
-                                  kManyWork / ((int64_t)d.max_blocks * d.page_tokens);
+  return rows >= kManyRows && (double)((rows + 7) / 8 * d.n_kv) * d.batch >=
+                                  (double)(kManyWork / ((int64_t)d.max_blocks * d.page_tokens));
 }
 
 
@@ -646,14 +646,19 @@ int kv4_attention_launch(const Kv4Dev& d, int head_dim, int max_new, const Kv4Te
   a.max_new = std::min(max_new, d.total);
   if (!d.indptr) a.max_new = std::min(a.max_new, d.each);
   a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)head_dim) : scale) * 1.4426950408889634f;
-  const int64_t row_blocks = ((int64_t)a.max_new * a.group + kRows - 1) / kRows;
-  const int64_t items = row_blocks * d.n_kv * d.batch;
-  if (row_blocks * kRows > INT_MAX || items > INT_MAX / kMaxSplit)
-    return op_fail(WPK_ERR_SHAPE, "too many query rows for one call");
+  // blocks of rows of the kernel that takes the call; row numbers fit 32 bits
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  const char* too_many = "too many query rows for one call (a closer max_new asks for fewer)";
+  if (rows > INT_MAX - kPrefillRows) return op_fail(WPK_ERR_SHAPE, too_many);
+  const bool many = many_rows(d, rows);
+  const int block = many ? kPrefillRows : kRows;
+  const int64_t row_blocks = (rows + block - 1) / block, blocks = row_blocks * d.n_kv;
+  if (blocks > INT_MAX / kMaxSplit / d.batch) return op_fail(WPK_ERR_SHAPE, too_many);
+  const int64_t items = blocks * d.batch;
   a.row_blocks = (int)row_blocks;
   cudaError_t e;
   const bool wide = head_dim == 128;
-  if (many_rows(d, (int64_t)a.max_new * a.group))
+  if (many)
     e = kv4_prefill_launch(d, head_dim, a.max_new, q, a.group, dtype, rope, a.scale_log2, out, s);
   else if (dtype == WPK_F32)
     e = wide ? choose<float, 128>(d, q, out, a, items, s) : choose<float, 64>(d, q, out, a, items, s);

@@ -20,7 +20,8 @@ int kv4_append_launch(const Kv4Dev& d, int head_dim, const Kv4Tensor& k, const K
 int kv4_attention_launch(const Kv4Dev& d, int head_dim, int max_new, const Kv4Tensor& q, int n_heads, int dtype,
                          const float* rope, float scale, const Kv4Tensor& out, cudaStream_t s);
 
-// Many query rows a kv head (kv4_prefill.cu); the checks are done.
+// Many query rows a kv head (kv4_prefill.cu), kPrefillRows a CTA; the checks are done.
+constexpr int kPrefillRows = 128;
 cudaError_t kv4_prefill_launch(const Kv4Dev& d, int head_dim, int max_new, const Kv4Tensor& q, int group, int dtype,
                                const float* rope, float scale_log2, const Kv4Tensor& out, cudaStream_t s);
 

@@ -39,7 +39,7 @@
 namespace wpk {
 namespace {
 
-constexpr int kM = 128;        // query rows of a CTA
+constexpr int kM = kPrefillRows;  // query rows of a CTA
 constexpr int kTile = 64;      // keys of a tile
 constexpr int kThreadsP = 256;
 constexpr int kSplits = 8;

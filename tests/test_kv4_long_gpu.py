@@ -39,3 +39,21 @@ def test_blocks_of_many_tiles(dtype, hd, sizes):
     assert torch.equal(got, got[:1].expand_as(got))
     for b in range(8):
         _near(got[0, b:b + 1], q64[b:b + 1], R.held(k64[b]), R.held(v64[b]), int(lens[b]) - 1, dtype, hd ** -0.5)
+
+
+def test_many_sequences_without_a_bound_of_their_runs():
+    """Without max_new any of 1100 sequences might bring all 66000 tokens; the answers are those with the bound."""
+    torch = _torch()
+    rng = np.random.default_rng(61)
+    B, n, kv, group, hd = 1100, 60, 8, 4, 64
+    c = W.KV4Cache(B, kv, hd, 64)
+    table, pos = _i32(rng.permutation(B)[:, None]), _i32(np.zeros(B))
+    ip = _i32(np.arange(B + 1) * n)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    rows = lambda heads: torch.randn(B * n, heads, hd, generator=g, device="cuda").bfloat16()  # noqa: E731
+    c.append(rows(kv), rows(kv), pos, table, indptr=ip)
+    q = rows(kv * group)
+    want = c.attention(q, pos, table, indptr=ip, max_new=n)
+    assert torch.equal(c.attention(q, pos, table, indptr=ip), want)
+    assert want.isfinite().all() and (want != 0).any(-1).all()
