@@ -433,6 +433,8 @@ class KV4Cache:
         import torch
 
         device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise WpkError(WPK_ERR_INVALID_ARG, f"the pages must be on a CUDA device, not {device}")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         if n_blocks <= 0 or n_kv_heads <= 0:

@@ -145,3 +145,8 @@ def test_plans_over_4_bit_pages():
     h = build(mode=W.WPK_PER_OP_GRAPH, kv_bits=16, page_tokens=32)
     assert W.wpk_workspace_size(h)[1] == shape.n_layers * 3 * 4 * shape.n_kv_heads * 32 * 256
     W.wpk_destroy(h)
+
+
+@pytest.mark.parametrize("device", ["cpu", "cpu:0", "meta"])
+def test_a_cache_is_on_a_cuda_device(device):
+    _refused(ARGS, lambda: W.KV4Cache(1, 1, 64, 16, device=device), "CUDA device", device)
