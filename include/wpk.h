@@ -452,6 +452,8 @@ enum { WPK_F32 = 0, WPK_BF16 = 1, WPK_F16 = 2 };
  *
  * Tensors are [token][head][head_dim] with a contiguous last dimension;
  * strides are in elements, multiples of 4, and pointers aligned to 4 elements.
+ * The strides of a tensor that a call writes are head_dim or more (where it has
+ * more than one token, or head).
  * The calls are stream-ordered, allocate nothing, keep nothing between calls
  * and can be captured.  Messages of failed calls: wpk_last_error(NULL). */
 typedef struct wpk_kv4_cache {

@@ -372,6 +372,14 @@ const char* tensor_problem(const Kv4Tensor& x, int dtype) {
   return nullptr;
 }
 
+// And of one that the call writes: rows of their own.
+const char* output_problem(const Kv4Tensor& x, int dtype, int total, int heads, int head_dim) {
+  const char* bad = tensor_problem(x, dtype);
+  if (bad) return bad;
+  if ((total > 1 && x.token < head_dim) || (heads > 1 && x.head < head_dim)) return "rows that are written must not overlap";
+  return nullptr;
+}
+
 }  // namespace
 
 // Checks what all calls share and fills the device view; returns WPK_OK or the
@@ -464,8 +472,8 @@ int wpk_kv4_read(const wpk_kv4_cache* cache, const int32_t* pos_dev, const int32
   const int rc = kv4_view(cache, pos_dev, indptr_dev, total, dtype, nullptr, 0, &d);
   if (rc) return rc;
   const Kv4Tensor k{k_dev, k_token_stride, k_head_stride}, v{v_dev, v_token_stride, v_head_stride};
-  const char* bad = tensor_problem(k, dtype);
-  if (!bad) bad = tensor_problem(v, dtype);
+  const char* bad = output_problem(k, dtype, total, cache->n_kv_heads, cache->head_dim);
+  if (!bad) bad = output_problem(v, dtype, total, cache->n_kv_heads, cache->head_dim);
   if (bad) return op_fail(WPK_ERR_INVALID_ARG, bad);
   if (total == 0) return WPK_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -488,7 +496,7 @@ int wpk_kv4_attention(const wpk_kv4_cache* cache, const int32_t* pos_dev, const 
   if (rc) return rc;
   const Kv4Tensor q{q_dev, q_token_stride, q_head_stride}, o{out_dev, out_token_stride, out_head_stride};
   const char* bad = tensor_problem(q, dtype);
-  if (!bad) bad = tensor_problem(o, dtype);
+  if (!bad) bad = output_problem(o, dtype, total, n_heads, cache->head_dim);
   if (bad) return op_fail(WPK_ERR_INVALID_ARG, bad);
   if (n_heads <= 0 || n_heads % cache->n_kv_heads)
     return op_fail(WPK_ERR_INVALID_ARG, "n_heads must be a positive multiple of n_kv_heads");

@@ -150,3 +150,11 @@ def test_plans_over_4_bit_pages():
 @pytest.mark.parametrize("device", ["cpu", "cpu:0", "meta"])
 def test_a_cache_is_on_a_cuda_device(device):
     _refused(ARGS, lambda: W.KV4Cache(1, 1, 64, 16, device=device), "CUDA device", device)
+
+
+@pytest.mark.parametrize("st", [(0, 64), (128, 0), (60, 64), (128, 32)])
+def test_rows_that_are_written_do_not_overlap(st):
+    c = _cache()
+    _refused(ARGS, lambda: W.wpk_kv4_read(c, P, 0, 2, P, st, P, (128, 64), 1), "overlap")
+    _refused(ARGS, lambda: W.wpk_kv4_read(c, P, 0, 2, P, (128, 64), P, st, 1), "overlap")
+    _refused(ARGS, lambda: W.wpk_kv4_attention(c, P, 0, 2, 1, P, (128, 64), 2, 1, P, st), "overlap")
