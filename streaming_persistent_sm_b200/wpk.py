@@ -595,14 +595,16 @@ class Engine:
         wpk_step(self.h, itp, out_tok.data_ptr(), logits.data_ptr() if logits is not None else 0, self._stream())
         return out_tok, logits
 
-    def sample(self, logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, **kw):
+    def sample(self, logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, out_tok=None, **kw):
         """A token per row of a step's (or prefill's) logits, drawn with the given uniform numbers; a
-        two-stage model's logits give a code per codebook, from uniform numbers and settings of the
-        same leading shape.  Arguments as for sample()."""
+        two-stage model's logits give a code per codebook, from uniform numbers and settings (and into
+        an out_tok) of the same leading shape.  Arguments as for sample()."""
         lead = logits.shape[:-1]
         flat = lambda x: None if x is None else x.reshape(-1)
+        if out_tok is not None and out_tok.is_contiguous():  # reshaping another one would write a copy
+            out_tok = out_tok.view(-1)
         out = sample(logits.reshape(-1, logits.shape[-1]), flat(uniform), flat(temperature), flat(top_k),
-                     flat(top_p), flat(min_p), **kw)
+                     flat(top_p), flat(min_p), out_tok, **kw)
         return tuple(x.reshape(lead) for x in out) if isinstance(out, tuple) else out.reshape(lead)
 
     def step_sampled(self, uniform, in_tok=None, **sampling):

@@ -103,3 +103,21 @@ def test_codes_of_a_two_stage_frame_are_drawn_from_its_logits():
         assert e.value.code == W.WPK_ERR_UNSUPPORTED
     finally:
         eng.close()
+
+
+def test_codes_go_into_the_tensor_given():
+    import torch
+
+    s = synth.TINY_TWO_STAGE
+    eng = W.Engine(s, synth.make_weights(s, seed=0), 2, 16)
+    try:
+        _, logits = eng.prefill(synth.make_prompts(s.backbone.vocab, 2, 4, 1), want_logits=True)
+        u = torch.rand(logits.shape[:2], device="cuda")
+        want = eng.sample(logits, u)
+        into = torch.zeros(logits.shape[:2], dtype=torch.int32, device="cuda")
+        got = eng.sample(logits, u, out_tok=into)
+        assert torch.equal(into, want) and got.data_ptr() == into.data_ptr() and got.shape == want.shape
+        with pytest.raises(W.WpkError):
+            eng.sample(logits, u, out_tok=torch.zeros(into.t().shape, dtype=torch.int32, device="cuda").t())
+    finally:
+        eng.close()
