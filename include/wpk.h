@@ -511,8 +511,9 @@ int wpk_kv4_attention(const wpk_kv4_cache *cache, const int32_t *pos_dev, const 
  * A temperature that is not > 0 takes the largest logit, the lowest id of equal
  * ones.  A logit of -inf masks its token.  A row with a NaN or +inf, or with
  * nothing but -inf, answers token -1, log-probability NaN and 0 kept tokens.
- * Masses are summed as whole multiples of 2^-45, so the result does not depend
- * on the order of the sums.  vocab <= 262144.
+ * Masses are summed as whole multiples of 2^-45, each weight's off from it by less
+ * than one, so the result does not depend on the order of the sums.
+ * vocab <= 262144.
  *   out_tok_dev     int32 [batch] (may be the in_tok_dev of the next wpk_step)
  *   out_logprob_dev fp32 [batch] or NULL: log of the token's share of the kept
  *                   mass

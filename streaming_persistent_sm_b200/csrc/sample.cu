@@ -22,9 +22,11 @@
 // whole multiple of 2^-45, so that sums do not depend on their order (shared
 // atomics, clusters of any size) and decisions at a border are those of the
 // definition.  B200 runs 64-bit arithmetic at half the 32-bit rate, and a weight
-// takes some 20 operations; the bulk of a row, of weights below 2^-14, is
-// computed in 32 bits with the exponent's rounding errors carried along: 2^-22
-// of such a weight, 2^-36 of the largest.
+// takes some 20 operations; the bulk of a row, of weights below 2^-24, is
+// computed in 32 bits with the exponent's rounding errors carried along, 2^-22
+// of such a weight, which is half of 2^-45.  (From 2^-14 down the same would save a
+// fifth of a row's time, but 2^17 such tokens shift a border by a hundredth of a
+// token: other draws than the definition's.)
 //
 // Measured, fp32 logits of 128256: one row 15 us, 48 rows with all filters 46 us, 128
 // with half of the tokens masked in half of the rows 85 us (0.6 TB/s of 66 MB); 32
@@ -102,9 +104,10 @@ __device__ __forceinline__ double exp_neg(double t) {
   return __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
 }
 
-// 2^-kTail: weights below it are computed in 32 bits.
-constexpr float kTail = 14.f;
-constexpr float kFar = 24.f;  // see tail_mass
+// Weights below 2^-kTail are computed in 32 bits, to half of 2^-45: 2^-22 of such a
+// weight.  See tail_mass for those below 2^-kFar.
+constexpr float kTail = 24.f;
+constexpr float kFar = 29.f;
 
 struct Weigh {  // weights of a row's tokens
   float zmax, log2_t, log2_t_rest;  // log2(e) / T and what its float leaves
@@ -118,7 +121,7 @@ struct Weigh {  // weights of a row's tokens
   // The mass of a token of log2_weight t < -kTail.  Down to 2^-kFar the exponent
   // is carried with its rounding errors (of the distance and of the product) and
   // split into a whole number and a rest below 1/2, so the error is ex2's, 2^-22.
-  // Below, t's own rounding (2^-19 of the weight) no longer counts.
+  // Below, t's own rounding (2^-18 of the weight) is less than 1/4 of 2^-45.
   __device__ __forceinline__ uint32_t tail_mass(float z, float t) const {
     float rest = t + 45.f, scale = 1.f, m;
     if (!(t < -kFar)) {
@@ -578,12 +581,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
   const bool filtered = by_k || by_p || floor_w > 0.0;
 
   // The mass of all tokens: what a row without filters draws from, and top-p
-  // alone is measured by.  For the latter, tokens of 2^-kFar and more fall into
+  // alone is measured by.  For the latter, tokens of 2^-kTail and more fall into
   // buckets of 1/80 of their weights' log2; a bucket sums up 2^13 times what its
   // tokens weigh against its near edge, rounded down (1 - x ln 2 <= 2^-x); 2^18
   // tokens fit 32 bits.
   constexpr float kSteps = 80.f;
-  static_assert(kFar * kSteps < kBins, "a bucket for every token");
+  static_assert(kTail * kSteps < kBins, "a bucket for every token");
   uint64_t all_mass = 0;
   if (!filtered || (by_p && !by_k)) {
     uint64_t v = 0;
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
           v += W.tail_mass(x[e], t);
         else if (x[e] > -INFINITY)
           v += W.heavy_mass(x[e]);
-        if (filtered && !(t < -kFar)) {
+        if (filtered && !(t < -kTail)) {
           const float at = fmaxf(-t, 0.f) * kSteps, edge = floorf(at);  // a NaN is 0
           atomicAdd(&S.count[(int)edge], (uint32_t)(8192.f - (at - edge) * (5678.27f / kSteps)));
         }
