@@ -159,7 +159,11 @@ typedef struct wpk_plan_cfg {
                            pages, so it needs WPK_PER_OP_GRAPH, CUDA-core decode,
                            token-by-token prefill (the automatic choices then)
                            and page_tokens % 16 == 0; no two-stage model, no
-                           wpk_prefill_slots                                    */
+                           wpk_prefill_slots.  It pays in memory, and in time for
+                           few sequences with long contexts: above 4 sequences
+                           the CUDA-core step takes several times as long as the
+                           tensor-core one of bf16 pages, and a prompt takes a
+                           step per token                                      */
 } wpk_plan_cfg;
 
 /* Host weights: bf16 bit patterns, row-major [out][in]. */
@@ -488,7 +492,12 @@ int wpk_kv4_read(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32
  * h / (n_heads / n_kv_heads).  scale 0 = 1 / sqrt(head_dim).  max_new: an upper
  * bound of the tokens of any one sequence (rows past it are left as they
  * were).  rope_dev rotates q on the way.  A query that sees no key, one past
- * the rope table and one of an idle sequence answer zeros. */
+ * the rope table and one of an idle sequence answer zeros.
+ * Sums and softmax statistics are fp32.  The products' operands are fp16: in bf16
+ * calls queries and weights are rounded to 2^-12 of themselves (with many query
+ * rows the cache's values too), in fp16 calls the weights are, in fp32 calls
+ * queries and weights keep 22 bits.  Logits and scale q have to stay below 1e35:
+ * beyond, finite numbers may answer NaN. */
 int wpk_kv4_attention(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32_t *indptr_dev, int total,
                       int max_new, const void *q_dev, int64_t q_token_stride, int64_t q_head_stride, int n_heads,
                       int dtype, const float *rope_dev, int rope_positions, float scale, void *out_dev,

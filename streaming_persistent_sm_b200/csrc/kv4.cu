@@ -12,11 +12,12 @@
 // sequence, the position, the page id, the angles), 2 us or so; the append's rows
 // are under way before their place is known.
 //
-// Measured, 8 kv heads of 64, bf16: 32 prompts of 496 tokens appended in 25 us
-// (2.2 TB/s), read back in 11; 48 single tokens in 6 us, one in 3.3 (latency).  The
-// append is bound by instructions: codes in 32 bits with bounds, and where a bound
-// says that a value may lie on a code's border, the exact decision; 16-bit values
-// lie on ties of their own scale so often that most warps take it somewhere.
+// Measured, 8 kv heads of 64, bf16: 32 prompts of up to 496 tokens appended in 23 us
+// (their 31 MB: 1.3 TB/s), read back in 10; 48 single tokens in 5 to 8 us, one in 3.1
+// (latency).  The append is bound by instructions: codes in 32 bits with bounds, and
+// where a bound says that a value may lie on a code's border, the exact decision;
+// 16-bit values lie on ties of their own scale so often that most warps take it
+// somewhere.
 #include <limits.h>
 
 #include "kv4.cuh"
@@ -254,7 +255,8 @@ __device__ __forceinline__ void load8(const T* p, float* f) {
   load4(p + 4, f + 4);
 }
 
-// Bound by bytes: a row comes in once and leaves as HD / 2 + 4 bytes.
+// A row comes in once and leaves as HD / 2 + 4 bytes; bound by the instructions of
+// its codes.
 template <typename T, int HD, bool kTurn>
 __global__ void __launch_bounds__(kThreadsKv4, kTurn ? 7 : 8)
     kv4_append_kernel(const Kv4Dev c, const T* __restrict__ k, int64_t k_tok, int64_t k_head, const T* __restrict__ v,
@@ -302,7 +304,8 @@ __device__ __forceinline__ void read_word(uint32_t w, uint32_t sz, T* out) {
   store4(out + HD / 2, x + 4);
 }
 
-// Bound by bytes: the append's traffic, the other way.
+// The append's traffic, the other way, in twice the time of its bytes: a row's codes
+// wait for the loads that say where they are, and leave as 8 bytes a store.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreadsKv4)
     kv4_read_kernel(const Kv4Dev c, T* __restrict__ k, int64_t k_tok, int64_t k_head, T* __restrict__ v, int64_t v_tok,

@@ -26,10 +26,10 @@
 // on timing.  Each warp streams its pages through its own ring of shared-memory
 // stages with 16-byte asynchronous copies; nothing spins.
 //
-// Bound by the instructions around the products, some 640 a warp's step, and for
+// Bound by the instructions around the products, some 680 a warp's step, and for
 // little work by latency.  Measured: 32 sequences of up to 8192 keys, 32 heads of 64
-// over 8 kv heads, bf16: 40 us (2.8 TB/s of cache); one of 131072, 64 heads of 128
-// over 8, fp16: 93 us (1.5 TB/s); one of 624: 7.7 us.
+// over 8 kv heads, bf16: 42 us (2.8 TB/s of cache); one of 131072, 64 heads of 128
+// over 8, fp16: 93 us (1.5 TB/s); one of 624: 7.6 us.
 #include <limits.h>
 #include <math.h>
 
@@ -53,9 +53,9 @@ constexpr int kMaxSplit = 16;
 // The tcgen05 kernel's calls: from 64 query rows a (sequence, kv head) on, where
 // this kernel would have much to do (blocks of 8 rows times the keys that a table
 // names).  Measured (us, this kernel / that one, bf16, heads of 64, 8 kv heads):
-// 16 sequences of 4096 keys: 48 rows 65 / 71, 64 rows 73 / 72, 128 rows 140 / 75;
-// of 512 keys: 96 rows 27 / 22, 128 rows 34 / 23; one of 4096: 128 rows 16 / 27.
-// fp16 and fp32 meet at 64 to 80 rows, heads of 128 at 56 to 64.
+// 16 sequences of 4096 keys: 48 rows 66 / 78, 64 rows 75 / 78, 128 rows 144 / 81;
+// of 512 keys: 64 rows 20 / 23, 96 rows 27 / 23, 128 rows 34 / 24; one of 4096:
+// 128 rows 17 / 28.  fp16 and fp32 meet at 64 to 80 rows, heads of 128 at 48 to 56.
 constexpr int kManyRows = 64;
 constexpr int64_t kManyWork = 1 << 20;
 bool many_rows(const Kv4Dev& d, int64_t rows) {

@@ -18,10 +18,10 @@
 //
 // Bound by the instructions around the products: for a tile the 128 rows' exp2
 // alone take an SM 512 cycles, the products of heads of 64 some 250, and a tile
-// takes 1600 of an SM that two CTAs share.  While S of a tile and O of the one
+// takes 1740 of an SM that two CTAs share.  While S of a tile and O of the one
 // before are computed the next tile is expanded; one block-wide barrier a tile.
 // Measured: 4 runs of 512 tokens on up to 4096, 32 heads of 64 over 8 kv heads,
-// bf16: 214 us (235 TFLOP/s); the codes of its cache fit L2.  Splits of the keys
+// bf16: 228 us (220 TFLOP/s); the codes of its cache fit L2.  Splits of the keys
 // over a cluster join as for few rows.
 #include <limits.h>
 #include <math.h>
@@ -801,9 +801,9 @@ cudaError_t launch(const Kv4Dev& d, const Kv4Tensor& q, const Kv4Tensor& o, Pref
   }
   // CTAs that share a block's keys: while the GPU (148 SMs) is not full, and once
   // more between one wave and two, where sequences of other lengths leave the last
-  // wave half empty (512 blocks of 3000 keys on average: 233 us whole, 211 in two,
-  // 278 in four, since a CTA's start costs as much as 4 tiles; 8 blocks of 4096 keys
-  // in 8 parts each 27 us, in 16 31 us)
+  // wave half empty (512 blocks of 3000 keys on average: 250 us whole, 228 in two,
+  // 296 in four, since a CTA's start costs as much as 4 tiles; 8 blocks of 4096 keys
+  // in 8 parts each 28 us, in 16 4 us more)
   const int64_t tiles = ((int64_t)d.max_blocks * d.page_tokens + kTile - 1) / kTile, wave = 148 * G::kPerSm;
   a.split = 1;
   while (a.split < kSplits && tiles >= a.split * 8 &&

@@ -28,10 +28,11 @@
 // fifth of a row's time, but 2^17 such tokens shift a border by a hundredth of a
 // token: other draws than the definition's.)
 //
-// Measured, fp32 logits of 128256: one row 15 us, 48 rows with all filters 46 us, 128
-// with half of the tokens masked in half of the rows 85 us (0.6 TB/s of 66 MB); 32
-// rows of 2048: 6.5 us.  Latency bounds it: the barriers between a row's passes, and
-// for a large top-k or a flat row the one CTA that sorts.
+// Measured, fp32 logits of 128256 (three inputs each): one row with top-p 11 to 23 us,
+// 48 rows with all filters 31 to 66, 128 with most of the tokens masked in half of the
+// rows 68 to 85 (0.8 to 1 TB/s of 66 MB); 32 rows of 2048: 6.7.  Latency bounds it: the
+// barriers between a row's passes, the 64-bit weights under top-p, and for a large
+// top-k or a flat row the one CTA that sorts.
 #include <limits.h>
 #include <math.h>
 
@@ -947,7 +948,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) wpk_sample_kernel(const Sampl
     if (by_mass) {
       const double want = ceil((double)p * (double)sum);
       target = min(want > 1.0 ? (uint64_t)want : (uint64_t)1, sum);
-      // as reach_p, of the mass that top-k leaves
+      // tokens beyond it together weigh less than half of the 1 - p that is left out:
+      // no more than vocab times what one at the distance weighs
       reach = temperature *
               (logf(2.f * A.vocab / (1.f - fmaxf(p, 0.f))) - logf((float)((double)sum / kOne)) + 0.1f);
     } else {

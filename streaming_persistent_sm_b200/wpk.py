@@ -466,7 +466,8 @@ class KV4Cache:
         """Causal attention of the new tokens' queries q [total][n_heads][head_dim] over the pages,
         which hold the new tokens' keys and values already (append them first).  ``rope`` rotates q
         on the way.  ``max_new`` bounds the tokens of one sequence (default: total, or total / batch
-        without ``indptr``); a close bound starts fewer thread blocks."""
+        without ``indptr``).  Give a close bound: it starts fewer thread blocks, and a loose one may
+        choose the kernel for many rows a sequence where there are few."""
         return self._calls.attention(q, pos, block_table, indptr, max_new, rope, scale, out)
 
 
