@@ -494,7 +494,7 @@ int wpk_kv4_read(const wpk_kv4_cache *cache, const int32_t *pos_dev, const int32
  * were).  rope_dev rotates q on the way.  A query that sees no key, one past
  * the rope table and one of an idle sequence answer zeros.
  * Sums and softmax statistics are fp32.  The products' operands are fp16: in bf16
- * calls queries and weights are rounded to 2^-12 of themselves (with many query
+ * calls queries and weights are rounded to 2^-11 of themselves (with many query
  * rows the cache's values too), in fp16 calls the weights are, in fp32 calls
  * queries and weights keep 22 bits.  Logits and scale q have to stay below 1e35:
  * beyond, finite numbers may answer NaN. */

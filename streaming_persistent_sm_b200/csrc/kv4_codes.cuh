@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t v_key_exp(float s, float y) {
 // at most, a value keeps all of fp16's digits.
 constexpr uint32_t kSpread = 12;
 
-// What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-12), V's
+// What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-11 at most), V's
 // codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
 // that the output's rounding is off, relative, of random values).  fp16: Q to 22
 // bits, V centred.  fp32: K centred and P to 22 bits too, and a step's own sums,

@@ -7,7 +7,7 @@
 // HD/2 + 4j, 4j + 1, ...).  For S = Q K^T K is K-major, for O = P V the same layout
 // of V is MN-major: nothing is transposed.  What the operands hold depends on what
 // the type has to keep:
-//  * bf16: the values s c + z rounded to fp16 (2^-12, as Q and P), times a power of
+//  * bf16: the values s c + z rounded to fp16 (off by 2^-11 at most, as Q and P), times a power of
 //    two that follows K's largest value in the tile and V's largest so far (each
 //    key's own, where they differ much);
 //  * fp16, fp32: the codes, which are exact (odd nibbles at 16 times their value);
