@@ -11,7 +11,8 @@
 // nibble), exactly, so one AND makes an operand of two codes; with the bits of
 // 1024 above it, it is 1024 + c (1024 + 16 c), and a subtraction leaves d.  V
 // takes the centred codes: a sum over thousands of tokens all of one sign would
-// lose what the centred one keeps (1.2e-3 against 2e-4 at 131072 tokens, fp16).
+// lose what the centred one keeps (1.2e-3 against 2e-4 at 131072 tokens, fp16, before
+// each step had sums of its own).
 //
 // One warp takes 64 keys at a time for up to 8 query rows: S = Q K^T as
 // m16n8k16 products (rows 0-7 Q rounded to fp16, rows 8-15 what the rounding
@@ -29,7 +30,7 @@
 // Bound by the instructions around the products, some 680 a warp's step, and for
 // little work by latency.  Measured: 32 sequences of up to 8192 keys, 32 heads of 64
 // over 8 kv heads, bf16: 42 us (2.8 TB/s of cache); one of 131072, 64 heads of 128
-// over 8, fp16: 93 us (1.5 TB/s); one of 624: 7.6 us.
+// over 8, fp16: 95 us (1.5 TB/s); one of 624: 7.6 us.
 #include <limits.h>
 #include <math.h>
 
@@ -424,10 +425,8 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
 
     // O^T += V^T P^T, 16 keys at a time
     float own[2 * WPL][4];
-    if (P::kOwnSums) {
 #pragma unroll
-      for (int i = 0; i < 2 * WPL; ++i) own[i][0] = own[i][1] = own[i][2] = own[i][3] = 0.f;
-    }
+    for (int i = 0; i < 2 * WPL; ++i) own[i][0] = own[i][1] = own[i][2] = own[i][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t b0 = pack_f16(x[4 * k], x[4 * k + 1]), b1 = pack_f16(x[4 * k + 2], x[4 * k + 3]);
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
           uint32_t a23 = __byte_perm(w[i][2], w[i][3], half ? 0x7632 : 0x5410);
 #pragma unroll
           for (int pair = 0; pair < 2; ++pair) {
-            float(&d)[4] = P::kOwnSums ? own[4 * i + 2 * half + pair] : o[4 * i + 2 * half + pair];
+            float(&d)[4] = own[4 * i + 2 * half + pair];
             const uint32_t e0 = P::kCentreV ? centred_even(a01) : a01 & kEven;
             const uint32_t e1 = P::kCentreV ? centred_odd(a01) : a01 & kOdd;
             const uint32_t e2 = P::kCentreV ? centred_even(a23) : a23 & kEven;
@@ -478,16 +477,14 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<HD, WARPS>::kPerSm)
         }
       }
     }
-    if (P::kOwnSums) {
 #pragma unroll
-      for (int i = 0; i < 2 * WPL; ++i)
+    for (int i = 0; i < 2 * WPL; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float2 r = split(add2(pair(o[i][e], o[i][e + 1]), pair(own[i][e], own[i][e + 1])));
-          o[i][e] = r.x;
-          o[i][e + 1] = r.y;
-        }
-    }
+      for (int e = 0; e < 4; e += 2) {
+        const float2 r = split(add2(pair(o[i][e], o[i][e + 1]), pair(own[i][e], own[i][e + 1])));
+        o[i][e] = r.x;
+        o[i][e + 1] = r.y;
+      }
   }
   cp_wait<0>();
   const float2 lp = split(l2), pp = split(py2);

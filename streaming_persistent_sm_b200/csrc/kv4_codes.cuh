@@ -78,14 +78,15 @@ __device__ __forceinline__ uint32_t v_key_exp(float s, float y) {
 constexpr uint32_t kSpread = 12;
 
 // What a type's precision asks for.  bf16: Q and P rounded to fp16 (2^-11 at most), V's
-// codes as they are, a step's O in sums of its own (they add 5e-4 to the 1.7e-3
-// that the output's rounding is off, relative, of random values).  fp16: Q to 22
-// bits, V centred.  fp32: K centred and P to 22 bits too, and a step's own sums,
-// since the tensor pipe cuts off what its sums cannot hold.
+// codes as they are (they add 5e-4 to the 1.7e-3 that the output's rounding is off,
+// relative, of random values).  fp16: Q to 22 bits, V centred.  fp32: K centred and P
+// to 22 bits too.  All: the products of a step (few rows) or tile in sums of their own,
+// since the tensor pipe cuts off what its sums cannot hold: over 2^18 keys in one sum
+// fp16 answers came out 4e-3 too small.
 template <typename T>
 struct Keep {
   static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value, kFp32 = std::is_same<T, float>::value;
-  static constexpr bool kQLow = !kBf16, kPLow = kFp32, kCentreK = kFp32, kCentreV = !kBf16, kOwnSums = kBf16 || kFp32;
+  static constexpr bool kQLow = !kBf16, kPLow = kFp32, kCentreK = kFp32, kCentreV = !kBf16;
 };
 
 }  // namespace wpk

@@ -57,3 +57,32 @@ def test_many_sequences_without_a_bound_of_their_runs():
     want = c.attention(q, pos, table, indptr=ip, max_new=n)
     assert torch.equal(c.attention(q, pos, table, indptr=ip), want)
     assert want.isfinite().all() and (want != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_million_keys_in_one_block(dtype, hd):
+    """640 sequences of 2^20 keys (they share their pages) leave no keys to split: a warp sums 2^18 of them.  All rows
+    of V are the same, so the answer is that row.  It is off by half a step of the type, by the rounding of the
+    weights times V's scale (2^-11 for bf16 and fp16, 2^-21 for fp32, of the part s c), and by sums of up to 2^15 terms,
+    numerator and denominator, whose roundings to nearest have either sign: n of them add up to 8 sqrt(n) 2^-24 or
+    more with a probability below 1e-13.  Sums that are cut off instead lose n 2^-24 and more: 4e-3."""
+    torch = _torch()
+    n, B = 1 << 20, 640
+    dt = getattr(torch, dtype)
+    c = W.KV4Cache(n // 64, 1, hd, 64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    row = torch.full((hd,), 0.93, dtype=dt, device="cuda")
+    row[0] = -0.21
+    k = torch.randn(n, 1, hd, generator=g, device="cuda").to(dt)
+    table = torch.arange(n // 64, dtype=torch.int32, device="cuda")[None]
+    c.append(k, row.expand(n, 1, hd).contiguous(), _i32([0]), table)
+    q = torch.randn(B, 4, hd, generator=g, device="cuda").to(dt)
+    got = c.attention(q, _i32([n - 1] * B), table.repeat(B, 1)).double().cpu().numpy()
+    want = R.held(row.double().cpu().numpy())
+    half = torch.finfo(dt).eps / 2
+    weight, sums = 2.0 ** -21 if dtype == "float32" else 2.0 ** -11, 8 * 2.0 ** 7.5 * 2.0 ** -24
+    part = want - want.min()
+    tol = half * np.abs(want) + weight * part + 2 * sums * (part + abs(want.min()) + np.abs(want))
+    assert (np.abs(got - want) <= tol).all(), float(np.abs(got - want).max())
