@@ -427,7 +427,8 @@ enum { WPK_F32 = 0, WPK_BF16 = 1, WPK_F16 = 2 };
 /* A paged KV cache held in 4 bits (one layer's).  Each row - the K or the V of
  * one token and kv head, head_dim values - is held as 4-bit codes c with a
  * scale s and an offset z (bf16 each), x ~ s c + z:
- *   z = the largest bf16 number <= min x,
+ *   z = the largest bf16 number <= min x (the lowest one, -3.39e38, where there
+ *       is none),
  *   s = the bf16 number next to (max x - z) / 15 (ties to even),
  *   c = (x - z) / s rounded to a whole number (ties to even), within 0..15
  *       (0 where s is 0);
